@@ -424,6 +424,113 @@ int spec_read_bandwidth(const void* buf, size_t bytes, uint64_t* sink, void* str
  */
 int spec_lds_atomic_probe(int pattern, int iters, uint64_t* sink, void* stream);
 
+/*
+ * A key/value cache in 4 bits for the target model of a verification round,
+ * and the attention of the round's new tokens over it.  A round scores
+ * n = gamma + 1 tokens per sequence (the last committed one and the gamma
+ * drafts) against everything the sequence holds; on rejection only the valid
+ * length moves (SSD summary, AMD MI300X part: rollback of the KV cache), and
+ * the next round's tokens overwrite the rejected ones' places.
+ *
+ * The format.  A vector of `dim` numbers is cut into blocks of 32.  A block
+ * holds one byte e, its scale s = 2^(e - 127), and a 4-bit code per number:
+ * bit 3 the sign, bits 0-2 one of the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * With a = the block's largest magnitude, s is the smallest power of two with
+ * a <= 7 s (from there on the largest number would be nearer to a code of the
+ * next scale), clamped to 3 <= e <= 252 so that every value is a normal,
+ * finite float and bfloat16; the code is the nearest value to x / s, ties to
+ * the even code, at most 6.  A block that holds a NaN or an infinity gets
+ * e = 255 and reads back as 32 NaN.
+ *
+ * The cache.  `data` [pages][heads][spec_cache_page_bytes(page, dim)] bytes, on a
+ * 16-byte boundary; page = tokens per page: 32, 64, 128 or 256; dim: 64, 128
+ * or 256; heads = key/value heads.  The record of one page and head holds, for
+ * token r of the page and number d of its vector,
+ *   the key codes: byte r * dim/2 + d/2, the even d in the low half;
+ *   from byte page * dim/2 on the value codes, so that one lane of the
+ *     attention finds its share of 4 tokens side by side: tile r/16 of 8 dim
+ *     bytes, in it [(r%16)/4][d / (dim/16)][r%4] pieces of dim/32 bytes;
+ *   from byte page * dim on the key scales: byte r * dim/32 + d/32;
+ *   after them the value scales: tile r/16 of dim/2 bytes, in it [d/32][r%16].
+ * `table` [B][table_len] int32: position t of sequence b lies in page
+ * table[b][t / page].  Entries of pages a call does not need are not read.  Two
+ * sequences may share pages they do not both write.
+ *
+ * Positions.  Token i of sequence b in a call is at position len[b] - lag + i,
+ * len [B] int32 (NULL: zeros).  After a verification len = out_len and
+ * lag = 1: out_len counts the token just drawn, which is not in the cache yet
+ * and is the first of the next round's tokens.  count [B] int32 (NULL: n
+ * everywhere) says how many of the n tokens sequence b has; rows behind them
+ * are neither read nor written.
+ *
+ * Errors.  B < 0, n < 1, heads < 1, pages < 0, table_len < 0, a page or dim
+ * that is not listed, table_len * page > 2^30, B * n > 2^24, sizes whose work
+ * items do not fit 31 bits (B * n * heads_q * dim > 2^34; B * heads * row groups of 16 > 2^24), a
+ * negative stride, lag outside {0, 1}, a NULL required pointer, `data` or an output off its
+ * 16-byte boundary: SPEC_EINVAL; an unknown dtype: SPEC_EDTYPE.  B == 0 is a
+ * no-op.  Found on the device, and confined to the sequence: a
+ * first position below 0, a count outside [0, n], or tokens past
+ * table_len * page positions (a range error), and a page outside [0, pages).
+ *
+ * spec_cache_append quantises the new tokens' keys and values into the cache.
+ *   k, v: [B][n][heads][dim] of dtype, token t = b * n + i at element
+ *     t * k_stride (v_stride); heads * dim numbers lie side by side.
+ *   status [B] int32 (nullable): 0, 1 for a range error (nothing of the
+ *     sequence is written), 2 for a bad page (the tokens on it are not written).
+ * spec_cache_read writes what the cache holds of those positions to out_k and
+ *   out_v [B][n][heads][dim] of dtype, contiguous: exact in both dtypes.  All n
+ *   rows are NaN after a range error, the rows of a bad page's tokens are NaN.
+ * spec_cache_attention, after the round's append: query head c of token i,
+ *   c = h * (heads_q / heads) + j, gives
+ *     out = sum_t w_t V_t[h] / sum_t w_t,  w_t = exp(scale * q . K_t[h])
+ *   over the positions t that row i sees, and lse = log sum_t w_t.
+ *   - mask == NULL: t <= its own position;
+ *   - mask [B][n] uint64, n <= 64 (a draft tree): every t before the first new
+ *     token's position, and new token j iff bit j of mask[b][i] is set (bits at
+ *     or past count[b] are ignored);
+ *   - window > 0: only t > its own position - window (its index in the call,
+ *     not its depth in a tree); window == 0: no limit.
+ *   A row that sees nothing gives out = 0, lse = -inf.  A row that sees a
+ *   position with a NaN block (key or value), or one on a bad page, is NaN as
+ *   a whole, as are all n rows after a range error; what a row does not see
+ *   never reaches it.
+ *   q: [B][n][heads_q][dim] of dtype, tokens q_stride elements apart;
+ *   heads_q: a multiple of heads; scale finite;
+ *   out: [B][n][heads_q][dim] of dtype, contiguous; lse: [B][n][heads_q] float
+ *   (nullable).  Outputs must not overlap inputs.
+ *   Scores, the softmax's maximum and sum and the output are held in 32 bits;
+ *   bf16 calls round the weights to bf16 for the product with the values.
+ *   The workspace must be zero-filled before its first use and is left
+ *   ready for the next call, as spec_workspace_bytes() describes; a call's
+ *   workspace serves every call with as many or fewer sequences, tokens and
+ *   heads.  Results do not depend on which work-group finishes first.
+ */
+typedef struct spec_cache {
+  void* data;
+  const int32_t* table;
+  int pages;
+  int heads;
+  int page;
+  int dim;
+  int table_len;
+} spec_cache;
+
+/* Bytes of one page and head (0 for a page or dim that is not supported). */
+size_t spec_cache_page_bytes(int page, int dim);
+
+int spec_cache_append(const spec_cache* cache, const void* k, const void* v, int dtype,
+                      int64_t k_stride, int64_t v_stride, const int32_t* len, int lag,
+                      const int32_t* count, int B, int n, int32_t* status, void* stream);
+int spec_cache_read(const spec_cache* cache, const int32_t* len, int lag, const int32_t* count,
+                    int B, int n, void* out_k, void* out_v, int dtype, int32_t* status,
+                    void* stream);
+/* 0 for B == 0 or arguments spec_cache_attention would reject. */
+size_t spec_cache_attention_workspace_bytes(int B, int n, int heads_q, int heads, int dim);
+int spec_cache_attention(const spec_cache* cache, const void* q, int dtype, int64_t q_stride,
+                         int heads_q, const int32_t* len, int lag, const int32_t* count, int B,
+                         int n, float scale, int window, const uint64_t* mask, void* out,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* A static, human-readable description of a status code. */
 const char* spec_status_str(int status);
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import math
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +25,8 @@ EXPORTED = ("spec_workspace_bytes", "spec_verify", "spec_verify_saguaro",
             "spec_verify_ex", "spec_synthetic_busy", "spec_verify_noalloc", "spec_read_bandwidth",
             "spec_lds_atomic_probe",
             "spec_synth_draft", "spec_synth_rows", "spec_ssd_prespeculate", "spec_ssd_advance",
+            "spec_cache_page_bytes", "spec_cache_append", "spec_cache_read",
+            "spec_cache_attention_workspace_bytes", "spec_cache_attention",
             "spec_status_str")
 
 
@@ -32,6 +35,13 @@ class SpecOptions(ctypes.Structure):
     _fields_ = [("saguaro", ctypes.c_int), ("eps", ctypes.c_float), ("early", ctypes.c_int),
                 ("temperature", ctypes.c_void_p), ("cand", ctypes.c_void_p),
                 ("hit", ctypes.c_void_p), ("cand_idx", ctypes.c_void_p), ("top_p", ctypes.c_float)]
+
+
+class SpecCache(ctypes.Structure):
+    """struct spec_cache (see spec_verify.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int),
+                ("heads", ctypes.c_int), ("page", ctypes.c_int), ("dim", ctypes.c_int),
+                ("table_len", ctypes.c_int)]
 
 
 class SpecDiag(ctypes.Structure):
@@ -98,6 +108,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.spec_lds_atomic_probe.restype = i32
     lib.spec_verify_noalloc.argtypes = verify_args[:-3] + [vp]
     lib.spec_verify_noalloc.restype = i32
+    i64, cache = ctypes.c_int64, ctypes.POINTER(SpecCache)
+    lib.spec_cache_page_bytes.argtypes = [i32, i32]
+    lib.spec_cache_page_bytes.restype = sz
+    lib.spec_cache_append.argtypes = [cache, vp, vp, i32, i64, i64, vp, i32, vp, i32, i32, vp, vp]
+    lib.spec_cache_append.restype = i32
+    lib.spec_cache_read.argtypes = [cache, vp, i32, vp, i32, i32, vp, vp, i32, vp, vp]
+    lib.spec_cache_read.restype = i32
+    lib.spec_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.spec_cache_attention_workspace_bytes.restype = sz
+    lib.spec_cache_attention.argtypes = [cache, vp, i32, i64, i32, vp, i32, vp, i32, i32, f32, i32,
+                                         vp, vp, vp, vp, sz, vp]
+    lib.spec_cache_attention.restype = i32
     lib.spec_status_str.argtypes = [i32]
     lib.spec_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -497,6 +519,166 @@ def spec_verify_predict(draft_logits, target_logits, draft_tokens, u_accept, u_s
                        u_sample, temperature, in_len, out, diag, workspace, stream,
                        eps if saguaro else 0.0, pred)
     return out, pred
+
+
+class QuantCache:
+    """A key/value cache in 4 bits (see spec_verify.h): ``data`` uint8
+    [pages, heads, spec_cache_page_bytes(page, dim)], ``table`` int32 [B, table_len],
+    the page of every ``page`` positions of each sequence.  The tensors are the
+    caller's; entries of ``table`` may change between calls."""
+
+    __slots__ = ("data", "table", "page", "dim", "_c")
+
+    def __init__(self, data, table, page: int, dim: int):
+        import torch
+        nbytes = spec_cache_page_bytes(page, dim)
+        if not nbytes:
+            raise ValueError(f"page is 32, 64, 128 or 256 and dim 64, 128 or 256, got {page} and {dim}")
+        if data.dtype != torch.uint8 or data.dim() != 3 or data.shape[2] != nbytes:
+            raise ValueError(f"data is uint8 [pages, heads, {nbytes}], got {data.dtype} {tuple(data.shape)}")
+        if table.dtype != torch.int32 or table.dim() != 2:
+            raise ValueError(f"table is int32 [B, table_len], got {table.dtype} {tuple(table.shape)}")
+        _check_dev(data, table)
+        if table.device != data.device:
+            raise ValueError("data and table must be on one device")
+        self.data, self.table, self.page, self.dim = data, table, page, dim
+        self._c = SpecCache(data.data_ptr(), table.data_ptr(), data.shape[0], data.shape[1], page, dim,
+                            table.shape[1])
+
+    @property
+    def heads(self) -> int:
+        return self.data.shape[1]
+
+
+def new_cache(pages: int, heads: int, dim: int, table, page: int = 64) -> QuantCache:
+    """A QuantCache with a pool of ``pages`` zero-filled pages on the device of ``table`` [B, table_len]."""
+    import torch
+    data = torch.zeros((pages, heads, spec_cache_page_bytes(page, dim)), dtype=torch.uint8, device=table.device)
+    return QuantCache(data, table, page, dim)
+
+
+def spec_cache_page_bytes(page: int, dim: int) -> int:
+    return int(load_library().spec_cache_page_bytes(page, dim))
+
+
+CacheRows = collections.namedtuple("CacheRows", "k v")
+AttentionOut = collections.namedtuple("AttentionOut", "out lse")
+
+
+def _token_stride(name: str, x, heads: int, dim: int) -> int:
+    """Elements between the tokens of x [B, n, heads, dim], whose heads lie side by side."""
+    if x.dim() != 4 or x.shape[2] != heads or x.shape[3] != dim:
+        raise ValueError(f"{name} is [B, n, {heads}, {dim}], got {tuple(x.shape)}")
+    if x.is_contiguous():
+        return heads * dim
+    B, n = x.shape[:2]
+    s = x.stride()
+    if s[3] != 1 or (heads > 1 and s[2] != dim) or (B > 1 and n > 1 and s[0] != n * s[1]):
+        raise ValueError(f"{name}: the numbers and heads of a token must lie side by side and the tokens of "
+                         f"[B, n] a constant stride apart, got strides {s}")
+    return s[1] if n > 1 else s[0]
+
+
+def _check_cache_call(cache: QuantCache, B: int, n: int, ints, rest):
+    """Types, shapes and devices of a cache call's arrays: ``ints`` are int32 [B]."""
+    import torch
+    dev = cache.data.device
+    if cache.table.shape[0] != B:
+        raise ValueError(f"the table has {cache.table.shape[0]} sequences, the call {B}")
+    for t in ints:
+        if t is not None:
+            if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B:
+                raise ValueError(f"length, count and status are int32 [{B}], got {t.dtype} {tuple(t.shape)}")
+            if t.device != dev or not t.is_contiguous():
+                raise ValueError("every tensor must be a contiguous tensor on the cache's device")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError("every tensor must be on the cache's device")
+
+
+def _cache_launch(f, dev, stream, *args):
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, _stream_handle(stream, dev))
+    else:   # a launch goes to the current device
+        with torch.cuda.device(dev):
+            st = f(*args, _stream_handle(stream, dev))
+    if st != SPEC_OK:
+        raise SpecError(st)
+
+
+def spec_cache_append(cache: QuantCache, k, v, length=None, lag: int = 0, count=None, status=None, stream=None):
+    """Quantise the keys and values k, v [B, n, heads, dim] of the new tokens
+    into the cache, at positions length - lag onwards (see spec_verify.h).
+    ``count`` int32 [B]: how many of the n tokens each sequence has.  Returns
+    ``status`` (int32 [B], or None if none was given)."""
+    ks = _token_stride("k", k, cache.heads, cache.dim)
+    vs = _token_stride("v", v, cache.heads, cache.dim)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must share shape and dtype")
+    B, n = k.shape[:2]
+    _check_cache_call(cache, B, n, (length, count, status), (k, v))
+    _cache_launch(load_library().spec_cache_append, cache.data.device, stream, ctypes.byref(cache._c), k.data_ptr(),
+                  v.data_ptr(), _dtype_code(k), ks, vs, _ptr(length), lag, _ptr(count), B, n, _ptr(status))
+    return status
+
+
+def spec_cache_read(cache: QuantCache, n: int, length=None, lag: int = 0, count=None, dtype=None, out=None,
+                    status=None, stream=None) -> CacheRows:
+    """The keys and values [B, n, heads, dim] that the cache holds at positions
+    length - lag onwards, in ``dtype`` (float32, or bfloat16 by default) or into
+    ``out`` (a CacheRows); rows behind ``count`` are left as they were."""
+    import torch
+    B, shape = cache.table.shape[0], (cache.table.shape[0], n, cache.heads, cache.dim)
+    if out is None:
+        new = lambda: torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.data.device)
+        out = CacheRows(new(), new())
+    if out.k.shape != shape or out.v.shape != shape or out.v.dtype != out.k.dtype or dtype not in (None, out.k.dtype):
+        raise ValueError(f"out holds two tensors {shape} of one dtype")
+    _check_dev(out.k, out.v)
+    _check_cache_call(cache, B, n, (length, count, status), out)
+    _cache_launch(load_library().spec_cache_read, cache.data.device, stream, ctypes.byref(cache._c), _ptr(length), lag,
+                  _ptr(count), B, n, out.k.data_ptr(), out.v.data_ptr(), _dtype_code(out.k), _ptr(status))
+    return out
+
+
+def spec_cache_attention_workspace_bytes(B: int, n: int, heads_q: int, heads: int, dim: int) -> int:
+    return int(load_library().spec_cache_attention_workspace_bytes(B, n, heads_q, heads, dim))
+
+
+def spec_cache_attention(cache: QuantCache, q, length=None, lag: int = 0, count=None, scale: float | None = None,
+                         window: int = 0, mask=None, out=None, lse: bool = False, workspace=None,
+                         stream=None) -> AttentionOut:
+    """Attention of the new tokens' queries q [B, n, heads_q, dim] over the
+    cache, which holds their keys and values already (see spec_verify.h).
+    scale: 1/sqrt(dim) by default; window: 0 = none; mask: int64 [B, n], bit j
+    of token i set if it sees new token j (None: causal); ``out``: an
+    AttentionOut to write, its lse None if not wanted; rows behind ``count`` are
+    left as they were."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError(f"q is [B, n, heads_q, dim], got {tuple(q.shape)}")
+    B, n, heads_q, dim = q.shape
+    qs = _token_stride("q", q, heads_q, cache.dim)
+    dev = cache.data.device
+    if out is None:
+        out = AttentionOut(torch.empty(q.shape, dtype=q.dtype, device=dev),
+                           torch.empty((B, n, heads_q), dtype=torch.float32, device=dev) if lse else None)
+    if out.out.shape != q.shape or out.out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if out.lse is not None and (out.lse.shape != q.shape[:3] or out.lse.dtype != torch.float32):
+        raise ValueError(f"lse is float32 {tuple(q.shape[:3])}")
+    if mask is not None and (mask.shape != q.shape[:2] or mask.dtype != torch.int64):
+        raise ValueError(f"mask is int64 {tuple(q.shape[:2])}")
+    if workspace is None:
+        workspace = new_workspace(spec_cache_attention_workspace_bytes(B, n, heads_q, cache.heads, cache.dim), dev)
+    _check_dev(out.out, out.lse, mask, workspace)
+    _check_cache_call(cache, B, n, (length, count), (q, out.out, out.lse, mask, workspace))
+    _cache_launch(load_library().spec_cache_attention, dev, stream, ctypes.byref(cache._c), q.data_ptr(),
+                  _dtype_code(q), qs, heads_q, _ptr(length), lag, _ptr(count), B, n,
+                  1.0 / math.sqrt(dim) if scale is None else scale, window, _ptr(mask), out.out.data_ptr(),
+                  _ptr(out.lse), workspace.data_ptr(), workspace.numel())
+    return out
 
 
 def bytes_algorithmic(B: int, gamma: int, V: int, dtype: int) -> int:

@@ -32,6 +32,10 @@ SOURCES = ["verify.hip", "predict.hip", "greedy.hip", "synthetic.hip", "readbw.h
 # committed traffic records to the code they were taken on).
 MEASURE = os.path.join(PKG, "measure")
 MEASURE_SOURCES = ["lds_probe.hip"]
+# The 4-bit key/value cache, outside csrc for the same reason: the digest is
+# the verification kernels' alone.
+CACHE = os.path.join(PKG, "cache")
+CACHE_SOURCES = ["cache.hip", "attention.hip"]
 
 
 def hipcc() -> str:
@@ -44,6 +48,7 @@ def hipcc() -> str:
 def command(out: str = LIB, extra=()) -> list[str]:
     srcs = [os.path.join(CSRC, s) for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
     srcs += [os.path.join(MEASURE, s) for s in MEASURE_SOURCES if os.path.exists(os.path.join(MEASURE, s))]
+    srcs += [os.path.join(CACHE, s) for s in CACHE_SOURCES if os.path.exists(os.path.join(CACHE, s))]
     return [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-Wall", "-Wno-unused-function",

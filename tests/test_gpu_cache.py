@@ -1,0 +1,660 @@
+"""The 4-bit cache's kernels (spec_cache_append, spec_cache_read,
+spec_cache_attention) against the float64 definition in oracle/cache.py.
+
+Every case prints its name before it touches the GPU.
+
+What append writes and read returns is exact: bytes and numbers are compared
+for equality.
+
+Bounds of the attention, per number, from the arithmetic (u = 2^-24, half a
+step of float32; h = half a step of the output type: 2^-8 for bfloat16, u for
+float32).  With A = sum w |v| / sum w and S1 = the largest scale * sum |q k|:
+* a score is a sum of dim products and a scaling, each off by at most u
+  relative to the terms' absolute sum: (dim + 8) u S1; a score's distance r
+  from the maximum, scaled to base 2, subtracted and exponentiated: 4 u r + 8 u;
+  both together, delta, change every weight by a factor of at most 1 +- 2 delta
+  and so the quotient by 4 delta A;
+* T weights are summed for the numerator and for the denominator, and partial
+  sums rescaled and joined: 2 (T + 40) u A;
+* bfloat16: the weights are rounded before the product, h A; the output is
+  rounded, h |out|.  float32: queries and weights are each cut into three
+  bfloat16 parts, which leaves at most 2^-24 of them: u S1 in the score, u A.
+* lse: delta + (T + 40) u + 2 u |lse|.
+"""
+import ctypes
+import itertools
+
+import numpy as np
+import pytest
+
+from oracle import cache as C
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+H = pytest.importorskip("gpu_harness")
+R = pytest.importorskip("rejection_sampling_verify_12_amd")
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+U = 2.0 ** -24
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+class Pool:
+    """A cache of random codes with every sequence's pages anywhere in the
+    pool; the codes and scales of what no sequence holds are random bytes, NaN
+    blocks among them, and unused table entries lie outside the pool."""
+
+    def __init__(self, rng, held, heads, page, dim, spare=3, table_len=None, scales=(122, 128)):
+        self.page, self.dim, self.heads, self.held = page, dim, heads, list(held)
+        need = [-(-t // page) for t in held]
+        self.pages = sum(need) + spare
+        order = rng.permutation(self.pages)
+        self.table_len = max(need + [1]) if table_len is None else table_len
+        self.table = np.full((len(need), self.table_len), -7, dtype=np.int32)
+        at = 0
+        self.data = rng.integers(0, 256, (self.pages, heads, page * (dim + dim // 16))).astype(np.uint8)
+        rows = [C.places(page, dim, r) for r in range(page)]
+        for b, m in enumerate(need):
+            self.table[b, :m] = order[at:at + m]
+            at += m
+            for p in range(m):
+                for r in range(min(page, held[b] - p * page)):
+                    for place in rows[r][2:]:
+                        self.data[self.table[b, p], :, place] = rng.integers(*scales, (len(place), heads))
+
+    def cache(self):
+        return R.QuantCache(dev(self.data), dev(self.table), self.page, self.dim)
+
+    def span(self, b, t0, t1):
+        return C.read_span(self.data, self.table[b], self.page, self.dim, t0, t1)
+
+
+def as64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def same(got, want):
+    got, want = np.asarray(got), np.asarray(want)
+    assert got.shape == want.shape
+    ok = (got == want) | (np.isnan(got) & np.isnan(want))
+    assert ok.all(), f"{(~ok).sum()} of {ok.size} differ, first at {np.argwhere(~ok)[0]}"
+
+
+def without_signed_zeros(data, page, dim):
+    """The bytes with every code 8 (minus zero) as 0, so that zeros compare equal."""
+    codes = data[..., : page * dim]
+    lo, hi = codes & 15, codes >> 4
+    out = data.copy()
+    out[..., : page * dim] = np.where(lo == 8, 0, lo) | (np.where(hi == 8, 0, hi) << 4)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# append and read
+
+APPENDS = [  # B, n, heads, dim, page, dtype, first positions, counts
+    (1, 1, 1, 64, 32, "bf16", [0], None),
+    (1, 1, 8, 128, 64, "bf16", [63], None),
+    (3, 9, 2, 128, 32, "bf16", [0, 27, 100], None),
+    (4, 17, 3, 64, 64, "f32", [5, 60, 0, 200], [17, 0, 1, 9]),
+    (2, 70, 1, 256, 32, "f32", [31, 90], [70, 33]),
+    (2, 300, 2, 256, 256, "bf16", [250, 1], None),
+    (5, 33, 5, 64, 128, "bf16", [0, 1, 2, 127, 128], [33, 32, 31, 0, 5]),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS, ids=lambda c: "B%d_n%d_h%d_d%d_p%d_%s" % c[:6])
+@pytest.mark.parametrize("lag", [0, 1])
+def test_append_writes_the_definition_and_nothing_else(case, lag):
+    B, n, heads, dim, page, dt, first, counts = case
+    H.say(f"[cache] append {case} lag={lag}")
+    rng = np.random.default_rng(B * 1000 + n)
+    cnt = counts or [n] * B
+    pool = Pool(rng, [f + c for f, c in zip(first, cnt)], heads, page, dim)
+    x = rng.standard_normal((2, B, n, heads, dim)) * 2.0 ** rng.integers(-20, 20, (2, B, n, heads, 1))
+    k, v = (dev(a, torch.float32).to(DT[dt]) for a in x)
+    cache = pool.cache()
+    status = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+    length = dev(np.array(first, dtype=np.int32) + lag)
+    count = None if counts is None else dev(np.array(counts, dtype=np.int32))
+    R.spec_cache_append(cache, k, v, length, lag=lag, count=count, status=status)
+    want = pool.data.copy()
+    k64, v64 = as64(k), as64(v)
+    for b in range(B):
+        for i in range(cnt[b]):
+            C.write(want, pool.table[b], page, dim, first[b] + i, k64[b, i], v64[b, i])
+    same(without_signed_zeros(cache.data.cpu().numpy(), page, dim), without_signed_zeros(want, page, dim))
+    assert status.tolist() == [0] * B
+    # and back, in both types; rows behind the counts stay as they were
+    for rt in ("bf16", "f32"):
+        out = R.CacheRows(*(torch.full((B, n, heads, dim), 77.0, dtype=DT[rt], device="cuda") for _ in range(2)))
+        R.spec_cache_read(cache, n, length, lag=lag, count=count, out=out, status=status)
+        assert status.tolist() == [0] * B
+        for got, src in zip(out, (k64, v64)):
+            g = as64(got)
+            for b in range(B):
+                same(g[b, :cnt[b]], C.values(*C.quantise(src[b, :cnt[b]])))
+                assert (g[b, cnt[b]:] == 77.0).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_every_bfloat16_quantises_as_defined(dim):
+    """All 65536 bit patterns, each in a block with other numbers of its
+    magnitude and below: ties, subnormals, the largest numbers, infinities, NaN."""
+    H.say(f"[cache] every bfloat16, dim {dim}")
+    bits = np.arange(65536, dtype=np.uint16)
+    vals = np.stack([bits, (bits & 0x8000) | np.maximum((bits & 0x7FFF).astype(int) - 0x60, 0).astype(np.uint16)], -1)
+    tokens = vals.reshape(-1, dim)                       # 131072 numbers
+    n = len(tokens)
+    k = dev(tokens.view(np.int16)).view(torch.bfloat16).view(1, n, 1, dim)
+    cache = R.new_cache(n // 64, 1, dim, torch.arange(n // 64, dtype=torch.int32, device="cuda").view(1, -1), page=64)
+    R.spec_cache_append(cache, k, k)
+    out = R.spec_cache_read(cache, n, dtype=torch.float32)
+    src = as64(k)[0, :, 0]
+    src = np.where(np.abs(src) < 2.0 ** -126, src, src)
+    want = C.values(*C.quantise(src))
+    same(as64(out.k)[0, :, 0], want)
+    same(as64(out.v)[0, :, 0], want)
+
+
+def test_float32_near_every_border():
+    """Numbers one step either side of the code borders and of the scale's border 7 s, for scales over the whole range."""
+    H.say("[cache] float32 borders")
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0, 6.0, 0.5], dtype=np.float32)
+    rows = []
+    for e in list(range(-126, -118)) + list(range(-60, 120, 7)) + [121, 122, 123, 124]:
+        s = np.float32(2.0) ** e
+        with np.errstate(over="ignore", under="ignore"):
+            b = (borders * s).astype(np.float32)
+            near = np.concatenate([b, np.nextafter(b, np.float32(np.inf)), np.nextafter(b, np.float32(0))])
+        for top in (6.0, 7.0):
+            for sign in (1, -1):
+                row = np.zeros(32, dtype=np.float32)
+                small = near[np.isfinite(near) & (np.abs(near) <= np.float32(top) * s)][:31]
+                row[1:1 + len(small)] = sign * small
+                row[0] = np.float32(top) * s
+                rows.append(row)
+        for x in (np.float32(7.0) * s, np.nextafter(np.float32(7.0) * s, np.float32(np.inf))):
+            row = np.zeros(32, dtype=np.float32)
+            row[3], row[4] = x if np.isfinite(x) else np.finfo(np.float32).max, s
+            rows.append(row)
+    rows.append(np.full(32, np.finfo(np.float32).max, dtype=np.float32))
+    while len(rows) % 2:
+        rows.append(np.zeros(32, dtype=np.float32))
+    x = np.stack(rows).reshape(-1, 64)
+    n = len(x)
+    k = dev(x).view(1, n, 1, 64)
+    pages = -(-n // 32)
+    cache = R.new_cache(pages, 1, 64, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1), page=32)
+    R.spec_cache_append(cache, k, k)
+    out = R.spec_cache_read(cache, n, dtype=torch.float32)
+    want = C.values(*C.quantise(x.astype(np.float64)))
+    same(as64(out.k)[0, :, 0], want)
+    same(as64(out.v)[0, :, 0], want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_takes_a_fused_projection_off_any_boundary(dt):
+    """k and v as slices of one projection whose storage starts one element in, and one expanded over the batch."""
+    H.say(f"[cache] strided append {dt}")
+    B, n, heads, dim, page = 2, 5, 3, 64, 32
+    wide = torch.randn(1 + B * n * 11 * dim, device="cuda").to(DT[dt])[1:].view(B, n, 11, dim)
+    k, v = wide[:, :, 4:7], wide[:, :, 7:10]
+    rng = np.random.default_rng(1)
+    pool = Pool(rng, [40, 20], heads, page, dim)
+    first = dev(np.array([35, 15], dtype=np.int32))
+    one, two = pool.cache(), pool.cache()
+    R.spec_cache_append(one, k, v, first)
+    R.spec_cache_append(two, k.contiguous(), v.contiguous(), first)
+    assert torch.equal(one.data, two.data)
+    same_token = k[:1, :1].expand(B, 1, heads, dim)
+    R.spec_cache_append(one, same_token, v[:, :1], first)
+    R.spec_cache_append(two, same_token.contiguous(), v[:, :1].contiguous(), first)
+    assert torch.equal(one.data, two.data)
+
+
+def test_range_errors_and_bad_pages_stay_with_their_sequence():
+    H.say("[cache] range errors and bad pages")
+    heads, dim, page, n = 2, 64, 32, 40
+    rng = np.random.default_rng(2)
+    first = np.array([0, -1, 90, 60, 30, 10], dtype=np.int32)
+    counts = np.array([40, 3, 40, 40, 41, -1], dtype=np.int32)   # ok; before 0; past 128; bad page; too many; negative
+    pool = Pool(rng, [40, 40, 128, 100, 100, 50], heads, page, dim, table_len=4)
+    pool.table[3, 2] = pool.pages                     # positions 64 .. 95 of sequence 3
+    cache = pool.cache()
+    k = torch.randn(6, n, heads, dim, device="cuda")
+    status = torch.full((6,), 9, dtype=torch.int32, device="cuda")
+    R.spec_cache_append(cache, k, k, dev(first), count=dev(counts), status=status)
+    assert status.tolist() == [0, 1, 1, 2, 1, 1]
+    want = pool.data.copy()
+    k64 = as64(k)
+    for b in (0, 3):
+        for i in range(counts[b]):
+            if not (b == 3 and 64 <= first[b] + i < 96):
+                C.write(want, pool.table[b], page, dim, int(first[b]) + i, k64[b, i], k64[b, i])
+    same(without_signed_zeros(cache.data.cpu().numpy(), page, dim), without_signed_zeros(want, page, dim))
+    out = R.CacheRows(*(torch.full((6, n, heads, dim), 5.0, device="cuda") for _ in range(2)))
+    status.fill_(9)
+    R.spec_cache_read(cache, n, dev(first), count=dev(counts), out=out, status=status)
+    assert status.tolist() == [0, 1, 1, 2, 1, 1]
+    for got in out:
+        g = as64(got)
+        assert np.isnan(g[[1, 2, 4, 5]]).all() and not np.isnan(g[0]).any()
+        bad = np.array([64 <= 60 + i < 96 for i in range(n)])
+        assert np.isnan(g[3, bad]).all() and not np.isnan(g[3, ~bad]).any()
+
+
+def test_empty_pool_and_empty_batch():
+    H.say("[cache] empty pool and batch")
+    table = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    cache = R.new_cache(0, 2, 64, table, page=32)
+    x = torch.randn(2, 3, 2, 64, device="cuda")
+    status = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    R.spec_cache_append(cache, x, x, status=status)
+    assert status.tolist() == [1, 1]
+    R.spec_cache_append(cache, x, x, count=zero, status=status)
+    assert status.tolist() == [0, 0]
+    got = R.spec_cache_attention(cache, x, lse=True)
+    assert got.out.isnan().all() and got.lse.isnan().all()
+    none = R.new_cache(1, 2, 64, torch.zeros((0, 1), dtype=torch.int32, device="cuda"), page=32)
+    R.spec_cache_append(none, x[:0], x[:0])
+    assert R.spec_cache_attention(none, x[:0]).out.shape == (0, 3, 2, 64)
+
+
+# ---------------------------------------------------------------------------
+# attention
+
+def check_attention(pool, q, got, first, counts, scale, window=0, mask=None, rows=None, guard=None):
+    """got against the definition for every row (or the listed (b, i, head))."""
+    B, n, hq, dim = q.shape
+    group = hq // pool.heads
+    q64, out, lse = as64(q), as64(got.out), None if got.lse is None else as64(got.lse)
+    bf = q.dtype == torch.bfloat16
+    h = 2.0 ** -8 if bf else U
+    spans = {}
+    worst = 0.0
+    for b, i, c in rows if rows is not None else itertools.product(range(B), range(n), range(hq)):
+        if i >= counts[b]:
+            if guard is not None:
+                assert (out[b, i, c] == guard).all() and (lse is None or lse[b, i, c] == guard)
+            continue
+        if b not in spans:
+            spans[b] = pool.span(b, 0, first[b] + counts[b])
+        t = np.arange(first[b] + counts[b])
+        ok = C.sees(first[b], i, counts[b], t, window, None if mask is None else int(mask[b, i]) & (2 ** 64 - 1))
+        K, V = (x[ok, c // group] for x in spans[b])
+        o, l, A, S1, r = C.attend(q64[b, i, c], K, V, scale)
+        where = f"sequence {b} token {i} head {c}"
+        if np.isnan(l):
+            assert np.isnan(out[b, i, c]).all() and (lse is None or np.isnan(lse[b, i, c])), where
+            continue
+        T = len(K)
+        delta = (dim + 8) * U * S1 + 4 * U * r + 8 * U + (0 if bf else U * S1)
+        tol = (4 * delta + 2 * (T + 40) * U + (h if bf else U)) * A + h * np.abs(o) + 1e-37
+        err = np.abs(out[b, i, c] - o)
+        assert (err <= tol).all(), f"{where}: off by {np.max(err / tol):.3g} bounds"
+        worst = max(worst, float(np.max(err / tol)))
+        if lse is not None:
+            if l == -np.inf:
+                assert lse[b, i, c] == -np.inf, where
+            else:
+                assert abs(lse[b, i, c] - l) <= delta + (T + 40) * U + 2 * U * abs(l), where
+    return worst
+
+
+def run_case(rng, B, n, heads, group, dim, page, dt, first, counts=None, window=0, mask=None, scale=None, lag=0, rows=None,
+             amplitude=2.0, workspace=None):
+    cnt = counts or [n] * B
+    pool = Pool(rng, [f + c for f, c in zip(first, cnt)], heads, page, dim)
+    q = dev(rng.standard_normal((B, n, heads * group, dim)) * amplitude, torch.float32).to(DT[dt])
+    out = R.AttentionOut(torch.full(q.shape, 55.0, dtype=q.dtype, device="cuda"),
+                         torch.full(q.shape[:3], 55.0, device="cuda"))
+    got = R.spec_cache_attention(pool.cache(), q, dev(np.array(first, dtype=np.int32) + lag), lag=lag,
+                                 count=None if counts is None else dev(np.array(counts, dtype=np.int32)), scale=scale,
+                                 window=window, mask=None if mask is None else dev(mask.astype(np.int64)), out=out,
+                                 workspace=workspace)
+    worst = check_attention(pool, q, got, first, cnt, dim ** -0.5 if scale is None else scale, window, mask, rows, guard=55.0)
+    H.say(f"[cache]   largest error {worst:.2f} of its bound")
+    return pool, q, got
+
+
+ATTENTION = [  # B, n, heads, group, dim, page, dtype, first, counts
+    (1, 1, 1, 1, 64, 32, "bf16", [0], None),                 # one token, nothing before it
+    (1, 1, 1, 1, 128, 64, "f32", [0], None),
+    (1, 1, 8, 4, 128, 64, "bf16", [31], None),               # a block filled to its end
+    (1, 1, 8, 4, 128, 64, "bf16", [32], None),               # and one past it
+    (2, 1, 2, 8, 128, 32, "bf16", [700, 1999], None),
+    (2, 1, 1, 16, 256, 64, "bf16", [127, 128], None),
+    (3, 5, 2, 2, 64, 32, "f32", [901, 0, 33], None),
+    (3, 5, 2, 3, 128, 128, "f32", [130, 1, 511], [5, 0, 3]),
+    (2, 7, 1, 5, 256, 256, "f32", [300, 15], None),
+    (4, 9, 2, 4, 128, 64, "bf16", [0, 1, 300, 1111], None),  # a verification round, gamma = 8
+    (4, 9, 1, 7, 256, 32, "bf16", [64, 65, 5, 222], [9, 1, 0, 8]),
+    (2, 17, 3, 1, 64, 64, "bf16", [95, 400], None),
+    (1, 64, 2, 4, 128, 64, "bf16", [77], None),
+    (2, 130, 1, 3, 128, 32, "bf16", [1, 40], [130, 77]),     # a piece of a prompt
+    (1, 200, 1, 2, 64, 32, "f32", [0], None),                # a whole prompt
+    (1, 65, 1, 16, 256, 64, "bf16", [10], None),
+    (33, 1, 3, 2, 64, 32, "bf16", list(range(0, 330, 10)), None),
+    (40, 3, 1, 1, 128, 32, "f32", [7 * b % 97 for b in range(40)], [b % 4 for b in range(40)]),
+]
+
+
+@pytest.mark.parametrize("case", ATTENTION, ids=lambda c: "B%d_n%d_h%dx%d_d%d_p%d_%s" % c[:7])
+@pytest.mark.parametrize("lag", [0, 1])
+def test_attention(case, lag):
+    H.say(f"[cache] attention {case} lag={lag}")
+    run_case(np.random.default_rng(sum(case[:6])), *case, lag=lag)
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 5000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_window(window, dt):
+    H.say(f"[cache] window {window} {dt}")
+    run_case(np.random.default_rng(window), 3, 6, 2, 3, 64 if dt == "f32" else 128, 32, dt, [0, 37, 401], window=window)
+
+
+def tree(rng, B, n):
+    """Every token sees itself and its ancestors."""
+    m = np.zeros((B, n), dtype=np.uint64)
+    for b in range(B):
+        for i in range(n):
+            m[b, i] = np.uint64(1) << np.uint64(i)
+            if i:
+                m[b, i] |= m[b, rng.integers(0, i)]
+    return m
+
+
+@pytest.mark.parametrize("n,dim,dt,window", [(3, 64, "bf16", 0), (24, 128, "bf16", 0), (64, 128, "bf16", 40), (64, 64, "f32", 0),
+                                             (31, 256, "bf16", 20), (33, 256, "f32", 0)])
+def test_draft_tree(n, dim, dt, window):
+    H.say(f"[cache] tree n={n} dim={dim} {dt} window={window}")
+    rng = np.random.default_rng(n)
+    run_case(rng, 3, n, 2, 2, dim, 32, dt, [0, 50, 333], mask=tree(rng, 3, n), window=window)
+    # bits at and past the count are ignored, and rows may see later tokens
+    m = rng.integers(0, 2 ** 63, (3, n)).astype(np.uint64) * np.uint64(2) + np.uint64(1)
+    run_case(rng, 3, n, 1, 3, dim, 32, dt, [9, 31, 100], counts=[n, max(1, n // 2), 1], mask=m, window=window)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_that_see_nothing(dt):
+    """A mask without bits before which nothing is cached, and one whose window cuts the rest off."""
+    H.say(f"[cache] empty rows {dt}")
+    rng = np.random.default_rng(8)
+    mask = np.array([[0, 1, 0, 8], [0, 0, 0, 0], [0, 2, 0, 4]], dtype=np.uint64)
+    _, _, got = run_case(rng, 3, 4, 1, 2, 64, 32, dt, [0, 0, 70], mask=mask)
+    assert got.lse[1].eq(-np.inf).all() and got.out[1].eq(0).all() and got.out[0, 0].eq(0).all()
+    _, _, got = run_case(rng, 3, 4, 1, 2, 64, 32, dt, [70, 70, 70], mask=mask, window=1)
+    assert got.lse[0, 0].eq(-np.inf).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 8.0, 1e-30])
+def test_scale(scale):
+    H.say(f"[cache] scale {scale}")
+    for dt in ("bf16", "f32"):
+        run_case(np.random.default_rng(9), 2, 3, 2, 2, 128, 32, dt, [10, 200], scale=scale)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_far_scores(dt):
+    """Scores of hundreds: weights that vanish and one that carries the row, its place early, late and in between."""
+    H.say(f"[cache] far scores {dt}")
+    run_case(np.random.default_rng(10), 4, 2, 1, 4, 128, 32, dt, [64, 200, 450, 1000], amplitude=200.0)
+
+
+def test_long_context_in_one_sequence():
+    """A context long enough to be split over many work-groups, compared on some rows."""
+    H.say("[cache] long context")
+    rng = np.random.default_rng(11)
+    pool = Pool.__new__(Pool)
+    page, dim, heads, T = 256, 128, 2, 40000 + 5
+    pool.page, pool.dim, pool.heads = page, dim, heads
+    pool.pages = -(-T // page) + 2
+    pool.table_len = -(-T // page)
+    pool.table = rng.permutation(pool.pages)[None, : pool.table_len].astype(np.int32)
+    pool.data = rng.integers(0, 256, (pool.pages, heads, page * (dim + dim // 16))).astype(np.uint8)
+    pool.data[..., page * dim:] = rng.integers(122, 128, (pool.pages, heads, page * dim // 16))
+    for dt in ("bf16", "f32"):
+        q = dev(rng.standard_normal((1, 5, 8, dim)) * 2, torch.float32).to(DT[dt])
+        got = R.spec_cache_attention(pool.cache(), q, dev(np.array([T - 5], dtype=np.int32)), lse=True)
+        check_attention(pool, q, got, [T - 5], [5], dim ** -0.5, rows=[(0, i, c) for i in (0, 4) for c in (0, 3, 5, 7)])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nan_reaches_only_the_rows_that_see_it(dt):
+    """NaN blocks in keys and in values of new tokens: rows before them, rows
+    whose mask or window leaves them out and other heads stay finite."""
+    H.say(f"[cache] NaN blocks {dt}")
+    rng = np.random.default_rng(12)
+    heads, dim, page, n = 2, 64, 32, 6
+    pool = Pool(rng, [50 + n, 31 + n, 9 + n], heads, page, dim)
+
+    def spoil(b, t, h, part, blk):
+        at = C.places(page, dim, t % page)[2 + part][blk]
+        pool.data[pool.table[b, t // page], h, at] = C.NAN_SCALE
+
+    spoil(0, 52, 0, 0, 1)      # new token 2, head 0, keys
+    spoil(1, 33, 1, 1, 0)      # new token 2, head 1, values
+    spoil(2, 4, 0, 1, 1)       # a cached token, values
+    q = dev(rng.standard_normal((3, n, 4, dim)), torch.float32).to(DT[dt])
+    first = [50, 31, 9]
+    for window, mask in ((0, None), (3, None), (0, np.array([[1, 3, 7, 8, 16, 36]] * 3, dtype=np.uint64))):
+        got = R.spec_cache_attention(pool.cache(), q, dev(np.array(first, dtype=np.int32)), window=window,
+                                     mask=None if mask is None else dev(mask.astype(np.int64)), lse=True)
+        check_attention(pool, q, got, first, [n] * 3, dim ** -0.5, window, mask)
+        assert got.out[0, :2].isfinite().all() and got.out[1, :2].isfinite().all() and got.out[0, :, 2:].isfinite().all()
+    # queries that are not finite stay with their row
+    q[0, 1, 2, 5], q[1, 0, 0, 0] = float("nan"), float("inf")
+    clean = R.spec_cache_attention(pool.cache(), torch.where(q.isfinite(), q, 0), dev(np.array(first, dtype=np.int32)))
+    got = R.spec_cache_attention(pool.cache(), q, dev(np.array(first, dtype=np.int32)))
+    assert got.out[0, 1, 2].isnan().all() and got.out[1, 0, 0].isnan().all()
+    keep = torch.ones(q.shape[:3], dtype=torch.bool, device="cuda")
+    keep[0, 1, 2] = keep[1, 0, 0] = False
+    assert torch.equal(torch.nan_to_num(got.out[keep], 3.0), torch.nan_to_num(clean.out[keep], 3.0))
+
+
+def test_attention_range_errors_and_bad_pages():
+    H.say("[cache] attention: range errors and bad pages")
+    rng = np.random.default_rng(13)
+    heads, dim, page, n = 2, 64, 32, 6
+    pool = Pool(rng, [100, 100, 100, 100, 100, 100, 20], heads, page, dim, table_len=4)
+    pool.table[3, 1] = pool.pages                        # positions 32 .. 63 of sequence 3
+    pool.table[4, 3] = -1                                # positions 96 ..
+    first = np.array([94, -1, 123, 94, 94, 94, 14], dtype=np.int32)
+    counts = np.array([6, 6, 6, 6, 6, 7, 6], dtype=np.int32)
+    q = torch.randn(7, n, 4, dim, device="cuda")
+    got = R.spec_cache_attention(pool.cache(), q, dev(first), count=dev(counts), lse=True)
+    nan = np.isnan(as64(got.out)).all((2, 3))
+    assert nan.tolist() == [[False] * 6, [True] * 6, [True] * 6, [True] * 6, [False, False] + [True] * 4, [True] * 6, [False] * 6]
+    assert (np.isnan(as64(got.lse)).all(2) == nan).all()
+    ok = [(b, i, c) for b in (0, 3, 4, 6) for i in range(n) for c in range(4)]
+    check_attention(pool, q, got, first, [6] * 7, dim ** -0.5, rows=ok)
+    # a window that leaves the bad page out does not look at it
+    got = R.spec_cache_attention(pool.cache(), q, dev(first), count=dev(counts), window=31, lse=True)
+    check_attention(pool, q, got, first, [6] * 7, dim ** -0.5, window=31, rows=ok)
+    assert got.out[3].isfinite().all()
+
+
+def test_attention_takes_strided_queries():
+    H.say("[cache] strided queries")
+    rng = np.random.default_rng(14)
+    for dt in ("bf16", "f32"):
+        pool = Pool(rng, [300, 77], 2, 64, 128)
+        wide = torch.randn(1 + 2 * 5 * 10 * 128, device="cuda").to(DT[dt])[1:].view(2, 5, 10, 128)
+        q = wide[:, :, 1:9]
+        first = dev(np.array([295, 72], dtype=np.int32))
+        a = R.spec_cache_attention(pool.cache(), q, first)
+        b = R.spec_cache_attention(pool.cache(), q.contiguous(), first)
+        assert torch.equal(a.out, b.out)
+
+
+def test_results_repeat_and_the_workspace_is_left_ready():
+    """The same bits every time, on a workspace that larger and smaller calls used in between."""
+    H.say("[cache] repeated calls")
+    rng = np.random.default_rng(15)
+    pool = Pool(rng, [3000, 40, 700], 2, 64, 128)
+    cache = pool.cache()
+    first = dev(np.array([2991, 31, 691], dtype=np.int32))
+    q = torch.randn(3, 9, 8, 128, device="cuda").bfloat16()
+    ws = R.new_workspace(R.spec_cache_attention_workspace_bytes(3, 9, 8, 2, 128), q.device)
+    ref = R.spec_cache_attention(cache, q, first, lse=True, workspace=ws)
+    for _ in range(20):
+        got = R.spec_cache_attention(cache, q, first, lse=True, workspace=ws)
+        assert torch.equal(got.out, ref.out) and torch.equal(got.lse, ref.lse)
+        one = R.spec_cache_attention(cache, q[:, :1], first, workspace=ws)
+        assert one.out.isfinite().all()
+    fresh = R.spec_cache_attention(cache, q, first, lse=True)
+    assert torch.equal(fresh.out, ref.out) and torch.equal(fresh.lse, ref.lse)
+
+
+def test_streams_with_their_own_workspaces():
+    H.say("[cache] two streams")
+    rng = np.random.default_rng(16)
+    pool = Pool(rng, [2000, 900], 2, 64, 128)
+    cache = pool.cache()
+    q = [torch.randn(2, 5, 8, 128, device="cuda").bfloat16() for _ in range(2)]
+    first = dev(np.array([1995, 895], dtype=np.int32))
+    ref = [R.spec_cache_attention(cache, x, first) for x in q]
+    ws = [R.new_workspace(R.spec_cache_attention_workspace_bytes(2, 5, 8, 2, 128), x.device) for x in q]
+    out = [[R.AttentionOut(torch.empty_like(x), None) for _ in range(8)] for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for r in range(8):
+        for s, x, w, o in zip(streams, q, ws, out):
+            with torch.cuda.stream(s):
+                R.spec_cache_attention(cache, x, first, out=o[r], workspace=w)
+    torch.cuda.synchronize()
+    for o, want in zip(out, ref):
+        assert all(torch.equal(x.out, want.out) for x in o)
+    # an explicit stream, not the current one
+    s = streams[0]
+    got = R.spec_cache_attention(cache, q[0], first, out=out[0][0], workspace=ws[0], stream=s)
+    s.synchronize()
+    assert torch.equal(got.out, ref[0].out)
+
+
+def test_a_captured_round_replays_with_new_lengths():
+    """append, attention and read captured in one graph; between replays the
+    lengths and inputs change and eager calls run on other buffers."""
+    H.say("[cache] graph replays")
+    rng = np.random.default_rng(17)
+    B, n, heads, dim, page = 3, 4, 2, 64, 32
+    pool = Pool(rng, [500] * B, heads, page, dim)
+    cache, eager = pool.cache(), pool.cache()
+    k, v = (torch.randn(B, n, heads, dim, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(B, n, heads * 3, dim, device="cuda").bfloat16()
+    length = torch.zeros(B, dtype=torch.int32, device="cuda")
+    out = R.AttentionOut(torch.empty_like(q), torch.empty(q.shape[:3], device="cuda"))
+    back = R.CacheRows(torch.empty_like(k), torch.empty_like(v))
+    ws = R.new_workspace(R.spec_cache_attention_workspace_bytes(B, n, heads * 3, heads, dim), q.device)
+
+    def round_(c, o, w, rows):
+        R.spec_cache_append(c, k, v, length, lag=1)
+        R.spec_cache_attention(c, q, length, lag=1, out=o, workspace=w)
+        R.spec_cache_read(c, n, length, lag=1, out=rows)
+
+    length.fill_(1)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        round_(cache, out, ws, back)
+    torch.cuda.synchronize()
+    eager.data.copy_(cache.data)                          # both caches have seen the first round
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        round_(cache, out, ws, back)
+    for r in range(6):
+        length.copy_(torch.tensor([1 + 37 * r, 1 + 80 * r, 490 - 5 * r], dtype=torch.int32))
+        for x in (k, v, q):
+            x.normal_()
+        g.replay()
+        e = R.AttentionOut(torch.empty_like(q), torch.empty(q.shape[:3], device="cuda"))
+        erows = R.CacheRows(torch.empty_like(k), torch.empty_like(v))
+        round_(eager, e, None, erows)
+        torch.cuda.synchronize()
+        assert torch.equal(out.out, e.out) and torch.equal(out.lse, e.lse), f"replay {r}"
+        assert torch.equal(back.k, erows.k) and torch.equal(back.v, erows.v) and torch.equal(cache.data, eager.data)
+
+
+def test_a_page_past_four_gigabytes():
+    """Offsets in the pool that need more than 32 bits."""
+    H.say("[cache] large pool")
+    heads, dim, page = 8, 256, 256
+    nbytes = R.spec_cache_page_bytes(page, dim) * heads
+    pages = (5 << 30) // nbytes
+    table = torch.tensor([[pages - 1, 3]], dtype=torch.int32, device="cuda")
+    cache = R.QuantCache(torch.zeros((pages, heads, nbytes // heads), dtype=torch.uint8, device="cuda"), table, page, dim)
+    k, v = (torch.randn(1, 300, heads, dim, device="cuda").bfloat16() for _ in range(2))
+    R.spec_cache_append(cache, k, v)
+    got = R.spec_cache_read(cache, 300, dtype=torch.float32)
+    same(as64(got.k)[0], C.values(*C.quantise(as64(k)[0])))
+    same(as64(got.v)[0], C.values(*C.quantise(as64(v)[0])))
+    small = R.new_cache(2, heads, dim, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), page=page)
+    R.spec_cache_append(small, k, v)
+    q = torch.randn(1, 300, heads * 2, dim, device="cuda").bfloat16()
+    assert torch.equal(R.spec_cache_attention(cache, q).out, R.spec_cache_attention(small, q).out)
+
+
+def test_a_round_after_a_rejection_overwrites_the_rejected_tokens():
+    """Append, attend, verify and roll back by the length alone: what the next
+    round sees equals a cache that never held the rejected tokens."""
+    H.say("[cache] rollback")
+    rng = np.random.default_rng(18)
+    B, gamma, V, heads, dim, page = 5, 3, 64, 2, 64, 32
+    n = gamma + 1
+    pool = Pool(rng, [200] * B, heads, page, dim)
+    cache = pool.cache()
+    length = dev(np.array([1, 30, 32, 33, 100], dtype=np.int32))
+    keep = []                                             # what each sequence committed
+    for r in range(4):
+        k, v = (torch.randn(B, n, heads, dim, device="cuda").bfloat16() for _ in range(2))
+        q = torch.randn(B, n, heads * 2, dim, device="cuda").bfloat16()
+        R.spec_cache_append(cache, k, v, length, lag=1)
+        got = R.spec_cache_attention(cache, q, length, lag=1, lse=True)
+        first = (length - 1).tolist()
+        pool.data = cache.data.cpu().numpy()
+        check_attention(pool, q, got, first, [n] * B, dim ** -0.5)
+        p = torch.randn(B, n, V, device="cuda")
+        out = R.spec_verify(p, torch.randn(B, n, V, device="cuda"), torch.randint(0, V, (B, gamma), dtype=torch.int32, device="cuda"),
+                            torch.rand(B, gamma, device="cuda"), torch.rand(B, n, device="cuda"), 1.0, in_len=length)
+        for b, a in enumerate(out.accepted.tolist()):
+            assert a >= 0
+            keep += [(b, first[b] + i, C.values(*C.quantise(as64(k)[b, i])), C.values(*C.quantise(as64(v)[b, i])))
+                     for i in range(a + 1)]
+        length = out.out_len
+    for b, t, k, v in keep:
+        gk, gv = C.read_span(cache.data.cpu().numpy(), pool.table[b], page, dim, t, t + 1)
+        same(gk[0], k)
+        same(gv[0], v)
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    H.say("[cache] refusals")
+    cache = R.new_cache(4, 2, 64, torch.zeros((3, 2), dtype=torch.int32, device="cuda"), page=32)
+    x = torch.randn(3, 2, 2, 64, device="cuda")
+    q = torch.randn(3, 2, 4, 64, device="cuda")
+    i32 = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for call in (lambda: R.spec_cache_append(cache, x[:2], x[:2]), lambda: R.spec_cache_append(cache, x, x[:, :1]),
+                 lambda: R.spec_cache_append(cache, x, x.bfloat16()), lambda: R.spec_cache_append(cache, x, x, i32.long()),
+                 lambda: R.spec_cache_append(cache, x, x, i32[:2]), lambda: R.spec_cache_append(cache, x.cpu(), x.cpu()),
+                 lambda: R.spec_cache_append(cache, x, x, i32.cpu()),
+                 lambda: R.spec_cache_read(cache, 2, out=R.CacheRows(x, x[:, :1])),
+                 lambda: R.spec_cache_read(cache, 2, dtype=torch.bfloat16, out=R.CacheRows(x, x)),
+                 lambda: R.spec_cache_attention(cache, q[..., :32]), lambda: R.spec_cache_attention(cache, q[:2]),
+                 lambda: R.spec_cache_attention(cache, q, mask=i32), lambda: R.spec_cache_attention(cache, q, out=R.AttentionOut(x, None)),
+                 lambda: R.spec_cache_attention(cache, q, out=R.AttentionOut(torch.empty_like(q), i32))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        R.spec_cache_append(cache, x.half(), x.half())
+    with pytest.raises(R.SpecError):
+        R.spec_cache_attention(cache, torch.randn(3, 2, 3, 64, device="cuda"))
+    with pytest.raises(R.SpecError):
+        R.spec_cache_attention(cache, q, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(R.SpecError):
+        R.spec_cache_append(cache, x, x, lag=2)
