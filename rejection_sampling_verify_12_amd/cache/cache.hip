@@ -7,26 +7,6 @@
 namespace sv {
 namespace {
 
-// Eight numbers of a row whose first lies anywhere its type's alignment allows.
-struct __attribute__((packed, aligned(2))) Bf16x8 { uint32_t w[4]; };
-struct __attribute__((packed, aligned(4))) F32x8 { float v[8]; };
-
-template <int DT>
-__device__ __forceinline__ void load_row8(const void* row, int64_t j, float (&x)[8]) {
-  if constexpr (DT == kBF16) {
-    const Bf16x8 t = *reinterpret_cast<const Bf16x8*>(static_cast<const uint16_t*>(row) + j);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = bf16_lo(t.w[e]);
-      x[2 * e + 1] = bf16_hi(t.w[e]);
-    }
-  } else {
-    const F32x8 t = *reinterpret_cast<const F32x8*>(static_cast<const float*>(row) + j);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = t.v[e];
-  }
-}
-
 // The page of position t, or -1.
 __device__ __forceinline__ int page_of(const CacheView& c, int b, int t) {
   const int p = c.table[(int64_t)b * c.table_len + (t >> c.page_log2)];
