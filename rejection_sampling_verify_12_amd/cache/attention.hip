@@ -54,9 +54,8 @@ constexpr int kTerms = DT == kBF16 ? 1 : 3;   // bfloat16 parts that a query or 
 
 // Waves per SIMD the registers of a variant leave room for.
 constexpr int waves_for(int D, int dt, int rt) {
-  const int terms = dt == kBF16 ? 1 : 3;
-  const int regs = rt * (D / 4 + terms * D / 8) + 96;
-  return regs <= 160 ? 3 : regs <= 250 ? 2 : 1;
+  const int regs = rt * (D / 4 + (dt == kBF16 ? 12 : 20)) + D / 4 + 64;
+  return regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
 }
 // Row tiles of a group, at most.
 constexpr int max_tiles(int D, int dt) { return dt == kBF16 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2); }
@@ -96,58 +95,68 @@ __device__ __forceinline__ Item item_of(const AttentionArgs& a, int b, int rg, i
   return it;
 }
 
-// A lane's share of a block: codes and scales of 2 tiles of 16 keys.
+// A lane's share of a block of 32 keys: codes and scales of 2 tiles of 16 keys.
 template <int D>
-struct Codes {
-  uint32_t k[2][D / 32], v[2][D / 32];
-  uint32_t ks[2], vs[2];
+struct Half {   // of the keys, or of the values
+  uint32_t w[2][D / 32];
+  uint32_t sc[2];
 };
 
 template <int D>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[D / 32]) {
+__device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t rs, int voff, int soff, uint32_t (&w)[D / 32]) {
   if constexpr (D == 64) {
-    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0);
     w[0] = t.x; w[1] = t.y;
   } else {
 #pragma unroll
     for (int x = 0; x < D / 128; ++x) {
-      const u32x4 t = reinterpret_cast<const u32x4*>(p)[x];
+      const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + 16 * x, soff, 0);
       w[4 * x] = t.x; w[4 * x + 1] = t.y; w[4 * x + 2] = t.z; w[4 * x + 3] = t.w;
     }
   }
 }
 
-// Block of keys p .. p + 31 of one page; page < 0: NaN blocks.
+// Where a lane's share lies in a record; the block's own place is scalar.
 template <int D>
-__device__ __forceinline__ void load_codes(const AttentionArgs& a, int page, int h, int p, int lane, Codes<D>& x) {
+struct Places {
+  int k, v, ks, vs;
+  __device__ __forceinline__ Places(int P, int lane) {
+    using F = Format<D>;
+    const int i = lane & 15, g = lane >> 4;
+    k = i * F::kRow + g * (D / 8);
+    v = F::values(P, 0, 0) + g * (2 * D) + i * (D / 8);
+    ks = F::key_scales(P, 0) + i * F::kBlocks + (D == 256 ? 2 * g : D == 128 ? g : g >> 1);
+    vs = F::value_scale(P, 0, 0) + i * (D / 16) / 32 * 16 + 4 * g;
+  }
+};
+
+// The record of one page and head, or no bytes for a page outside the pool.
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t record_rsrc(const AttentionArgs& a, int page, int h) {
+  const int bytes = Format<D>::record(1 << a.c.page_log2);
+  return chunk_rsrc(a.c.data + ((int64_t)max(page, 0) * a.c.heads + h) * bytes, page < 0 ? 0 : bytes);
+}
+template <int D>
+__device__ __forceinline__ void load_keys(__amdgpu_buffer_rsrc_t rs, int r, const Places<D>& at, Half<D>& x) {
   using F = Format<D>;
-  const int i = lane & 15, g = lane >> 4;
-  if (page >= 0) {
-    const int P = 1 << a.c.page_log2, r = p & (P - 1);
-    const uint8_t* rec = a.c.data + ((int64_t)page * a.c.heads + h) * F::record(P);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      load_words<D>(rec + F::keys(r + 16 * t) + (i * F::kRow + g * (D / 8)), x.k[t]);
-      const uint8_t* ks = rec + F::key_scales(P, r + 16 * t) + i * F::kBlocks;
-      if constexpr (D == 256) {
-        x.ks[t] = *reinterpret_cast<const uint16_t*>(ks + 2 * g);
-      } else {
-        x.ks[t] = ks[D == 128 ? g : g >> 1];
-      }
+  for (int t = 0; t < 2; ++t) {
+    load_words<D>(rs, at.k + 16 * t * F::kRow, r * F::kRow, x.w[t]);
+    if constexpr (D == 256) {
+      x.sc[t] = __builtin_amdgcn_raw_buffer_load_b16(rs, at.ks + 16 * t * F::kBlocks, r * F::kBlocks, 0);
+    } else {
+      x.sc[t] = __builtin_amdgcn_raw_buffer_load_b8(rs, at.ks + 16 * t * F::kBlocks, r * F::kBlocks, 0);
     }
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_values(__amdgpu_buffer_rsrc_t rs, int r, const Places<D>& at, Half<D>& x) {
+  using F = Format<D>;
+  // 16 tokens take as many bytes of values (scales) as of keys (scales).
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      load_words<D>(rec + F::values(P, r + 16 * t, 0) + (g * (2 * D) + i * (D / 8)), x.v[t]);
-      x.vs[t] = *reinterpret_cast<const uint32_t*>(rec + F::value_scale(P, r + 16 * t, 0) + (i * (D / 16) / 32 * 16 + 4 * g));
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) x.k[t][c] = x.v[t][c] = 0;
-      x.ks[t] = D == 256 ? 0xFFFFu : 0xFFu;
-      x.vs[t] = 0xFFFFFFFFu;
-    }
+  for (int t = 0; t < 2; ++t) {
+    load_words<D>(rs, at.v + 16 * t * F::kRow, r * F::kRow, x.w[t]);
+    x.sc[t] = __builtin_amdgcn_raw_buffer_load_b32(rs, at.vs + 16 * t * F::kBlocks, r * F::kBlocks, 0);
   }
 }
 
@@ -198,122 +207,134 @@ struct State {   // one wave's running result; a lane holds query (lane & 15) of
   float m[RT], l[RT];   // maximum (base 2), and the sum over the lane's own keys
 };
 
+// Whether a group's queries are kept in shared memory (else in registers).
+template <int DT, int RT>
+constexpr bool kQueriesShared = RT * kTerms<DT> > 1;
+
 template <int D, int DT, int RT>
 struct Rows {   // the group's queries
-  bf16x8 q[RT][D / 32][kTerms<DT>];
+  bf16x8 q[kQueriesShared<DT, RT> ? 1 : D / 32];
+  const u32x4* shared;   // [D / 32][RT][terms][64 lanes]
   int token[RT];
 };
 
+// Scores of a block: rows = keys, columns = queries.  rt's tile t holds keys
+// 16 t + 4 (lane / 16) + 0 .. 3 of query lane % 16.
 template <int D, int DT, int RT>
-__device__ __forceinline__ void attend_block(const AttentionArgs& a, const Item& it, int b, int p, int lane,
-                                             Codes<D>& x, const Rows<D, DT, RT>& rows, State<D, DT, RT>& st) {
+__device__ __forceinline__ void score_block(const Half<D>& x, const Rows<D, DT, RT>& rows, int lane, f32x4 (&s)[RT][2]) {
   constexpr int T = kTerms<DT>;
-  const int g = lane >> 4;
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const bool full = p + kBlock - 1 <= (a.mask ? it.s.pos - 1 : it.s.pos + it.tok0) &&
-                    (a.window == 0 || p > it.s.pos + it.tok1 - a.window);
-  // Keys with a NaN block (rare): bit 16 t + key of the tile.
-  uint32_t nan_keys = 0;
-  if (__any((int)(has_ff(x.ks[0]) | has_ff(x.ks[1]) | has_ff(x.vs[0]) | has_ff(x.vs[1])))) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    bf16x8 k[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      uint64_t k = __ballot(has_ff(x.ks[t]) != 0);
-      k |= k >> 32;
-      uint32_t keys = (uint32_t)(k | k >> 16) & 0xFFFFu;
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const bool bad = (x.vs[t] >> (8 * jj) & 255) == 255;
-        const uint64_t v = __ballot(bad);
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) keys |= (v >> (16 * gg) & 0xFFFF) ? 1u << (4 * gg + jj) : 0u;
-        // The row's weight says NaN; the value itself must not reach other rows.
-        if (bad) x.vs[t] = (x.vs[t] & ~(255u << (8 * jj))) | 127u << (8 * jj);
-      }
-      nan_keys |= keys << (16 * t);
+      const float sc = scale_of(D == 256 ? (c < 4 ? x.sc[t] & 255 : x.sc[t] >> 8) : x.sc[t]);
+      const uint32_t w = x.w[t][c];
+      k[t] = as_bf16x8(cvt_pair(w, sc, 0), cvt_pair(w, sc, 1), cvt_pair(w, sc, 2), cvt_pair(w, sc, 3));
     }
-  }
-  if (!full) {
-    // Places behind the last token hold anything: no scale of theirs may give an infinity.
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        if ((x.vs[t] >> (8 * jj) & 255) > 252) x.vs[t] = (x.vs[t] & ~(255u << (8 * jj))) | 127u << (8 * jj);
+      for (int e = T - 1; e >= 0; --e) {
+        bf16x8 q;
+        if constexpr (kQueriesShared<DT, RT>) {
+          q = __builtin_bit_cast(bf16x8, rows.shared[((c * RT + rt) * T + e) * 64 + lane]);
+        } else {
+          q = rows.q[c];
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[t], q, s[rt][t], 0, 0, 0);
       }
     }
   }
+}
 
-  f32x4 s[RT][2];
+// Keys of the block with a NaN block, bit 16 t + key of tile t (rare).  The
+// row's weight will say NaN; the value itself must not reach other rows, so
+// its scale is replaced.
+template <int D>
+__device__ __forceinline__ uint32_t find_nan_keys(uint32_t k0, uint32_t k1, uint32_t (&v)[2]) {
+  uint32_t found = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const float s0 = scale_of(x.ks[t] & 255), s1 = D == 256 ? scale_of(x.ks[t] >> 8) : s0;
+    uint64_t k = __ballot(has_ff(t ? k1 : k0) != 0);
+    k |= k >> 32;
+    uint32_t keys = (uint32_t)(k | k >> 16) & 0xFFFFu;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) s[rt][t] = zero;
+    for (int jj = 0; jj < 4; ++jj) {
+      const bool bad = (v[t] >> (8 * jj) & 255) == 255;
+      const uint64_t m = __ballot(bad);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const uint32_t w = x.k[t][c];
-      const float sc = (D == 256 && c >= 4) ? s1 : s0;
-      const bf16x8 k = as_bf16x8(cvt_pair(w, sc, 0), cvt_pair(w, sc, 1), cvt_pair(w, sc, 2), cvt_pair(w, sc, 3));
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int e = T - 1; e >= 0; --e)
-          s[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, rows.q[rt][c][e], s[rt][t], 0, 0, 0);
+      for (int gg = 0; gg < 4; ++gg) keys |= (m >> (16 * gg) & 0xFFFF) ? 1u << (4 * gg + jj) : 0u;
+      if (bad) v[t] = (v[t] & ~(255u << (8 * jj))) | 127u << (8 * jj);
     }
+    found |= keys << (16 * t);
   }
+  return found;
+}
 
-  bf16x8 w[RT][T];
+// Weights of a block and the running maximum and sum.  `masked`: some row does not see some key.
+template <int D, int DT, int RT>
+__device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& it, int b, int p, int lane, bool masked,
+                                            uint32_t nan_keys, const Rows<D, DT, RT>& rows, f32x4 (&s)[RT][2],
+                                            State<D, DT, RT>& st, bf16x8 (&w)[RT][kTerms<DT>]) {
+  const int g = lane >> 4;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    if (!full || nan_keys) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = s[rt][e >> 2][e & 3] * a.c2;
+    if (masked || nan_keys) {
       const int at = it.s.pos + rows.token[rt];
-      const int last = a.mask ? it.s.pos - 1 : at;
-      const uint64_t bits = (a.mask && rows.token[rt] < it.s.count) ? a.mask[(int64_t)b * a.c.n + rows.token[rt]] : 0;
+      const bool used = rows.token[rt] < it.s.count;
+      const int last = !used ? -1 : a.mask ? it.s.pos - 1 : at;
+      const uint64_t bits = (a.mask && used) ? a.mask[(int64_t)b * a.c.n + rows.token[rt]] : 0;
+      const int first = a.window > 0 ? at - a.window + 1 : 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int key = p + 16 * (e >> 2) + 4 * g + (e & 3);
-        bool sees = key <= last && rows.token[rt] < it.s.count;
-        if (a.mask && key >= it.s.pos && key < it.s.pos + it.s.count) sees = bits >> (key - it.s.pos) & 1;
-        if (a.window > 0) sees = sees && key > at - a.window;
-        const float v = (nan_keys >> (16 * (e >> 2) + 4 * g + (e & 3)) & 1) ? __uint_as_float(0x7FC00000u) : s[rt][e >> 2][e & 3];
-        s[rt][e >> 2][e & 3] = sees ? v : -INFINITY;
+        const int in = 16 * (e >> 2) + 4 * g + (e & 3), key = p + in, j = key - it.s.pos;
+        const bool sees = key >= first && (key <= last || (j >= 0 && j < it.s.count && (bits >> j & 1)));
+        if (nan_keys >> in & 1) x[e] = __uint_as_float(0x7FC00000u);
+        x[e] = sees ? x[e] : -INFINITY;
       }
     }
-    const f32x4 x0 = s[rt][0], x1 = s[rt][1];
-    float top = fmaxf(fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])), fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])));
+    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
     const auto max2 = [](float u, float v) { return fmaxf(u, v); };
     top = swap_combine<16>(top, max2);
-    top = swap_combine<32>(top, max2) * a.c2;
-    const float m = fmaxf(st.m[rt], top);
-    const float safe = m == -INFINITY ? 0.0f : m;
-    if (__any(m > st.m[rt])) {
-      const float alpha = exp2_fast(st.m[rt] - safe);
+    top = swap_combine<32>(top, max2);
+    if (__any(top > st.m[rt])) {
+      const float m = fmaxf(st.m[rt], top);
+      const float alpha = exp2_fast(st.m[rt] - (m == -INFINITY ? 0.0f : m));
       st.l[rt] *= alpha;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) st.o[rt][d] *= alpha;
       st.m[rt] = m;
     }
-    float pr[8];
+    const float safe = st.m[rt] == -INFINITY ? 0.0f : st.m[rt];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) pr[e] = exp2_fast(fmaf(s[rt][e >> 2][e & 3], a.c2, -safe));
-    st.l[rt] += ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
-    split8<T>(pr, w[rt]);
+    for (int e = 0; e < 8; ++e) x[e] = exp2_fast(x[e] - safe);
+    st.l[rt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    split8<kTerms<DT>>(x, w[rt]);
   }
+}
 
-  float vsc[2][4];
+// O^T += V^T P^T.  Numbers 2 d and 2 d + 1 of the lane's D / 16, for its 8 keys; token jj's codes are bytes
+// jj * D/32 on of the lane's share.
+template <int D, int DT, int RT>
+__device__ __forceinline__ void gather_block(const Half<D>& x, const bf16x8 (&w)[RT][kTerms<DT>], State<D, DT, RT>& st) {
+  constexpr int T = kTerms<DT>;
+  float sc[8];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int jj = 0; jj < 4; ++jj) vsc[t][jj] = scale_of(x.vs[t] >> (8 * jj) & 255);
-  // Numbers 2 d and 2 d + 1 of the lane's D / 16, for its 8 keys.  Token jj's
-  // codes are bytes jj * D/32 on of the lane's share.
+  for (int e = 0; e < 8; ++e) sc[e] = scale_of(x.sc[e >> 2] >> (8 * (e & 3)) & 255);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) {
     uint32_t y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int byte = (e & 3) * (D / 32) + d;
-      y[e] = cvt_pair(x.v[e >> 2][byte / 4], vsc[e >> 2][e & 3], byte % 4);
+      y[e] = cvt_pair(x.w[e >> 2][byte / 4], sc[e], byte % 4);
     }
     uint32_t even[4], odd[4];
 #pragma unroll
@@ -333,79 +354,107 @@ __device__ __forceinline__ void attend_block(const AttentionArgs& a, const Item&
   }
 }
 
-// D / 16 numbers of a row of the output.
-template <int D, int DT>
-__device__ __forceinline__ void store_row(void* out, int64_t at, const float (&v)[D / 16]) {
+// N numbers of a row of the output.
+template <int D, int DT, int N>
+__device__ __forceinline__ void store_numbers(void* out, int64_t at, const float (&v)[N]) {
   if constexpr (DT == kBF16) {
-    uint32_t w[D / 32];
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    for (int e = 0; e < N / 2; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
     uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at);
-    if constexpr (D == 64) {
+    if constexpr (N == 4) {
       *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
     } else {
 #pragma unroll
-      for (int e = 0; e < D / 128; ++e) reinterpret_cast<u32x4*>(p)[e] = u32x4{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]};
+      for (int e = 0; e < N / 8; ++e) reinterpret_cast<u32x4*>(p)[e] = u32x4{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]};
     }
   } else {
     f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at);
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) p[e] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+    for (int e = 0; e < N / 4; ++e) p[e] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
   }
 }
 
-__device__ __forceinline__ float ld_dev_f(const float* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Units in W equal runs (the first U % W have one more): the first unit of
+// run w, and the run of unit u.
+struct Runs {
+  int q, rem;
+  __device__ __forceinline__ Runs(int U, int W) : q(U / W), rem(U - U / W * W) {}
+  __device__ __forceinline__ int start(int w) const { return w * q + min(w, rem); }
+  __device__ __forceinline__ int of(int u) const {
+    const int wide = rem * (q + 1);
+    return u < wide ? u / (q + 1) : rem + (u - wide) / q;
+  }
+};
+
+// Parts of an item's result pass through the workspace past the caches that
+// work-groups on other dies do not share (cache policy sc1, as an agent-scope
+// atomic has it), 16 bytes at a time.
+constexpr int kDeviceScope = 16;
+__device__ __forceinline__ f32x4 ld_part(__amdgpu_buffer_rsrc_t rs, int byte) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, byte, 0, kDeviceScope));
 }
-__device__ __forceinline__ void st_dev_f(float* p, float v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void st_part(__amdgpu_buffer_rsrc_t rs, int byte, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, byte, 0, kDeviceScope);
+}
+__device__ __forceinline__ float ld_part1(__amdgpu_buffer_rsrc_t rs, int byte) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, byte, 0, kDeviceScope));
+}
+__device__ __forceinline__ void st_part1(__amdgpu_buffer_rsrc_t rs, int byte, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, byte, 0, kDeviceScope);
 }
 
-// Work-groups take equal runs of units: run w is [w U / W, (w + 1) U / W) of all
-// U units, ordered by sequence, row group, key/value head and key.  An item
-// (all keys of one group and head) that lies in one run is written at once;
-// otherwise each run's part goes to the workspace, and the last to arrive
-// joins the parts in order.  A run has at most two such parts, its first and its last.
+// A table entry through the scalar cache: the address is the wave's.
+__device__ __forceinline__ int scalar_at(const int32_t* p, int at) {
+  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[at];
+}
+
+// Work-groups take equal runs of units, ordered by sequence, row group,
+// key/value head and key.  An item (all keys of one group and head) that lies
+// in one run is written at once; otherwise each run's part goes to the
+// workspace, and the last to arrive joins the parts in order.  A run has at
+// most two such parts, its first and its last.
 template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kernel(AttentionArgs a) {
-  constexpr int R = 16 * RT, S = D / 16, kPart = R * (D + 2);
-  __shared__ float sums[kWaves][16][D + 4];
+  constexpr int R = 16 * RT, S = D / 16, kPart = R * (D + 2), T = kTerms<DT>;
+  constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = kQueriesShared<DT, RT> ? R * D * 2 * T : 0;
+  __shared__ __align__(16) char space[kSums > kQ ? kSums : kQ];   // the queries, then the waves' results
   __shared__ float tops[kWaves][R], totals[kWaves][R];
-  __shared__ int64_t scan[kWaves];
-  __shared__ int64_t found_start;
-  __shared__ int found_entry, is_last;
+  __shared__ int scan[kWaves], found_start, found_entry, is_last;
+  float (&sums)[kWaves][16][D + 4] = *reinterpret_cast<float (*)[kWaves][16][D + 4]>(space);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int heads = a.c.heads, entries = a.c.B * a.groups;
 
-  // Units before this thread's entries, and in all.
+  // Units of one head before this thread's entries, and in all (the host keeps them within 31 bits).
   const int per = (entries + kThreads - 1) / kThreads;
   const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
-  int64_t mine = 0;
+  int mine = 0;
   for (int e = e0; e < e1; ++e) mine += item_of(a, e / a.groups, e % a.groups, R).units;
-  int64_t before = mine;
+  int before = mine;
+#pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int64_t o = __shfl_up((long long)before, off);
+    const int o = __shfl_up(before, off);
     if (lane >= off) before += o;
   }
   if (lane == 63) scan[wave] = before;
   __syncthreads();
   before -= mine;
-  int64_t all = 0;
+  int all = 0;
+#pragma unroll
   for (int w = 0; w < kWaves; ++w) {
     if (w < wave) before += scan[w];
     all += scan[w];
   }
-  const int64_t U = all * heads;
-  const int64_t W = U < (int64_t)gridDim.x ? U : (int64_t)gridDim.x;
-  const int64_t run = blockIdx.x;
+  const int U = uni(all * heads), W = min(U, (int)gridDim.x), run = blockIdx.x;
   if (run >= W) return;   // the whole work-group
-  int64_t u = run * U / W;
-  const int64_t u1 = (run + 1) * U / W, u_begin = u;
+  const Runs runs(U, W);
+  int u = runs.start(run);
+  const int u1 = runs.start(run + 1), u_begin = u;
   if (before * heads <= u && u < (before + mine) * heads) {
-    int64_t start = before * heads;
+    int start = before * heads;
     for (int e = e0; e < e1; ++e) {
-      const int64_t units = (int64_t)item_of(a, e / a.groups, e % a.groups, R).units * heads;
+      const int units = item_of(a, e / a.groups, e % a.groups, R).units * heads;
       if (u < start + units) {
         found_entry = e;
         found_start = start;
@@ -415,32 +464,36 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     }
   }
   __syncthreads();
-  int entry = uni(found_entry);
-  int64_t entry_start = (int64_t)uni((uint64_t)found_start);
+  int entry = uni(found_entry), entry_start = uni(found_start);
+  const Places<D> places(1 << a.c.page_log2, lane);
+  const __amdgpu_buffer_rsrc_t parts = chunk_rsrc(a.parts, (int)(2 * gridDim.x * kPart * sizeof(float)));
 
   while (u < u1) {
     const int b = entry / a.groups, rg = entry % a.groups;
     const Item it = item_of(a, b, rg, R);
-    const int64_t entry_units = (int64_t)it.units * heads;
-    if (u >= entry_start + entry_units) {
-      entry_start += entry_units;
+    if (u >= entry_start + it.units * heads) {
+      entry_start += it.units * heads;
       ++entry;
       continue;
     }
-    const int h = (int)((u - entry_start) / it.units);
-    const int64_t u0 = entry_start + (int64_t)h * it.units;   // the item's first unit
-    const int k0 = (int)(u - u0);
-    const int k1 = (int)((u1 < u0 + it.units ? u1 : u0 + it.units) - u0);
+    const int h = (u - entry_start) / it.units;
+    const int u0 = entry_start + h * it.units;   // the item's first unit
+    const int k0 = u - u0, k1 = min(u1 - u0, it.units);
+    const int row0 = rg * R;
+    // Rows in use; all n tokens' after a range error.
+    const int used = min(R, (it.s.count < 0 ? a.c.n : it.s.count) * a.group - row0);
+    const auto place_of = [&](int r) {   // row r of the group in q and out, in rows of D
+      const int row = row0 + r, token = row / a.group;
+      return ((int64_t)b * a.c.n + token) * a.heads_q + h * a.group + (row - token * a.group);
+    };
 
     if (it.s.count < 0) {
       float nan[S];
 #pragma unroll
       for (int d = 0; d < S; ++d) nan[d] = __uint_as_float(0x7FC00000u);
-      for (int r = tid >> 4; r < R; r += 16) {
-        const int row = rg * R + r, token = row / a.group, head = h * a.group + row % a.group;
-        if (token >= a.c.n) break;
-        const int64_t at = ((int64_t)b * a.c.n + token) * a.heads_q + head;
-        store_row<D, DT>(a.out, at * D + (tid & 15) * S, nan);
+      for (int r = tid >> 4; r < used; r += 16) {
+        const int64_t at = place_of(r);
+        store_numbers<D, DT, S>(a.out, at * D + (tid & 15) * S, nan);
         if (a.lse && (tid & 15) == 0) a.lse[at] = nan[0];
       }
       u += 1;
@@ -449,55 +502,95 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
 
     Rows<D, DT, RT> rows;
     State<D, DT, RT> st;
+    rows.shared = reinterpret_cast<const u32x4*>(space);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = rg * R + rt * 16 + i, token = row / a.group, head = h * a.group + row % a.group;
+      const int row = row0 + rt * 16 + i, token = row / a.group, head = h * a.group + (row - token * a.group);
       rows.token[rt] = token;
-      const bool used = token < it.s.count && !a.zero;
+      const bool live = token < it.s.count && !a.zero;
       const int64_t at = ((int64_t)b * a.c.n + token) * a.q_stride + (int64_t)head * D + g * (D / 4);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
+        if (kQueriesShared<DT, RT> && (rt * (D / 32) + c) % kWaves != wave) continue;   // the waves share the work
         float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (used) load_row8<DT>(a.q, at + 8 * c, x);
+        if (live) load_row8<DT>(a.q, at + 8 * c, x);
         if (a.flip) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = -x[e];
         }
-        split8<kTerms<DT>>(x, rows.q[rt][c]);
+        bf16x8 q[T];
+        split8<T>(x, q);
+        if constexpr (kQueriesShared<DT, RT>) {
+#pragma unroll
+          for (int e = 0; e < T; ++e)
+            reinterpret_cast<u32x4*>(space)[((c * RT + rt) * T + e) * 64 + lane] = __builtin_bit_cast(u32x4, q[e]);
+        } else {
+          rows.q[c] = q[0];
+        }
       }
       st.m[rt] = -INFINITY;
       st.l[rt] = 0.0f;
 #pragma unroll
       for (int d = 0; d < S; ++d) st.o[rt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    if constexpr (kQueriesShared<DT, RT>) __syncthreads();
 
-    // The wave's blocks p = lo + 128 k + 32 wave below hi; codes are loaded one
-    // block ahead, page numbers two.
+    // The wave's blocks p = lo + 128 k + 32 wave below hi.  The next block's
+    // keys are loaded when this one's have been used, and so its values.
     const int32_t* table = a.c.table + (int64_t)b * a.c.table_len;
-    const int p1 = min(it.hi, it.lo + kUnitKeys * k1);
+    const int p1 = min(it.hi, it.lo + kUnitKeys * k1), P = 1 << a.c.page_log2;
     int p = it.lo + kUnitKeys * k0 + kBlock * wave;
-    const auto page_at = [&](int pos) {
-      if (pos >= p1) return -1;
-      const int page = table[pos >> a.c.page_log2];
+    const auto page_at = [&](int pos) {   // positions behind the run read the run's last page
+      const int page = scalar_at(table, min(pos, p1 - 1) >> a.c.page_log2);
       return (page >= 0 && page < a.c.pages) ? page : -1;
     };
     if (p < p1) {
-      Codes<D> x, y;
-      int next = uni(page_at(p));
-      load_codes<D>(a, next, h, p, lane, x);
-      next = uni(page_at(p + kUnitKeys));
-      for (; p < p1; p += kUnitKeys) {
-        if (p + kUnitKeys < p1) load_codes<D>(a, next, h, p + kUnitKeys, lane, y);
-        next = uni(page_at(p + 2 * kUnitKeys));
-        attend_block<D, DT, RT>(a, it, b, p, lane, x, rows, st);
-        x = y;
+      Half<D> k, v;
+      int page = page_at(p);
+      __amdgpu_buffer_rsrc_t rec = record_rsrc<D>(a, page, h);
+      load_keys<D>(rec, p & (P - 1), places, k);
+      load_values<D>(rec, p & (P - 1), places, v);
+      int next = page_at(p + kUnitKeys);
+      for (;;) {
+        const int pn = p + kUnitKeys;
+        const bool more = pn < p1;
+        f32x4 s[RT][2];
+        bf16x8 w[RT][T];
+        if (page < 0) {
+          k.sc[0] = k.sc[1] = D == 256 ? 0xFFFFu : 0xFFu;
+          v.sc[0] = v.sc[1] = 0xFFFFFFFFu;
+        }
+        const bool masked = p + kBlock - 1 > (a.mask ? it.s.pos - 1 : it.s.pos + it.tok0) ||
+                            (a.window > 0 && p <= it.s.pos + it.tok1 - a.window);
+        score_block<D, DT, RT>(k, rows, lane, s);
+        const uint32_t ks0 = k.sc[0], ks1 = k.sc[1];
+        rec = record_rsrc<D>(a, more ? next : -1, h);
+        load_keys<D>(rec, pn & (P - 1), places, k);
+        uint32_t nan_keys = 0;
+        if (__any((int)(has_ff(ks0) | has_ff(ks1) | has_ff(v.sc[0]) | has_ff(v.sc[1]))))
+          nan_keys = find_nan_keys<D>(ks0, ks1, v.sc);
+        if (masked) {
+          // Places behind the last token hold anything: no scale of theirs may give an infinity.
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t& x = v.sc[e >> 2];
+            if ((x >> (8 * (e & 3)) & 255) > 252) x = (x & ~(255u << (8 * (e & 3)))) | 127u << (8 * (e & 3));
+          }
+        }
+        weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, rows, s, st, w);
+        gather_block<D, DT, RT>(v, w, st);
+        if (!more) break;
+        load_values<D>(rec, pn & (P - 1), places, v);
+        p = pn;
+        page = next;
+        next = page_at(p + kUnitKeys);
       }
     }
 
     // Join the waves.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const auto add2 = [](float v, float w) { return v + w; };
+      const auto add2 = [](float x, float y) { return x + y; };
       st.l[rt] = swap_combine<32>(swap_combine<16>(st.l[rt], add2), add2);
       if (g == 0) {
         tops[wave][rt * 16 + i] = st.m[rt];
@@ -506,12 +599,13 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == it.units;
-    float* part = a.parts + (2 * run + (u == u_begin ? 0 : 1)) * kPart;
+    const int part = (2 * run + (u == u_begin ? 0 : 1)) * kPart;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt > 0) __syncthreads();   // sums is read by the tile before
       {
         float m = tops[0][rt * 16 + i];
+#pragma unroll
         for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][rt * 16 + i]);
         const float f = exp2_fast(st.m[rt] - (m == -INFINITY ? 0.0f : m));
 #pragma unroll
@@ -520,75 +614,86 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
           for (int d = 0; d < S; ++d) sums[wave][i][(4 * g + r) * S + d] = st.o[rt][d][r] * f;
       }
       __syncthreads();
-      const int row16 = tid >> 4, share = tid & 15;
-      float m = tops[0][rt * 16 + row16], l = 0.0f, v[S];
-      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][rt * 16 + row16]);
-      const float safe = m == -INFINITY ? 0.0f : m;
-      for (int w = 0; w < kWaves; ++w) l += totals[w][rt * 16 + row16] * exp2_fast(tops[w][rt * 16 + row16] - safe);
+      const int row16 = tid >> 4, share = tid & 15, r = rt * 16 + row16;
+      if (r < used) {
+        float m = tops[0][r], l = 0.0f, v[S];
 #pragma unroll
-      for (int d = 0; d < S; ++d)
-        v[d] = (sums[0][row16][share * S + d] + sums[1][row16][share * S + d]) + (sums[2][row16][share * S + d] + sums[3][row16][share * S + d]);
-      if (whole) {
-        const int row = rg * R + rt * 16 + row16, token = row / a.group, head = h * a.group + row % a.group;
-        if (token < it.s.count) {
-          const int64_t at = ((int64_t)b * a.c.n + token) * a.heads_q + head;
+        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][r]);
+        const float safe = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) l += totals[w][r] * exp2_fast(tops[w][r] - safe);
+#pragma unroll
+        for (int d = 0; d < S; ++d)
+          v[d] = (sums[0][row16][share * S + d] + sums[1][row16][share * S + d]) + (sums[2][row16][share * S + d] + sums[3][row16][share * S + d]);
+        if (whole) {
+          const int64_t at = place_of(r);
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
           for (int d = 0; d < S; ++d) v[d] *= inv;
-          store_row<D, DT>(a.out, at * D + share * S, v);
+          store_numbers<D, DT, S>(a.out, at * D + share * S, v);
           if (a.lse && share == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int d = 0; d < S; ++d) st_dev_f(part + (rt * 16 + row16) * D + share * S + d, v[d]);
-        if (share == 0) {
-          st_dev_f(part + R * D + rt * 16 + row16, m);
-          st_dev_f(part + R * D + R + rt * 16 + row16, l);
+          for (int d = 0; d < S; d += 4) st_part(parts, (part + r * D + share * S + d) * 4, f32x4{v[d], v[d + 1], v[d + 2], v[d + 3]});
+          if (share == 0) {
+            st_part1(parts, (part + R * D + r) * 4, m);
+            st_part1(parts, (part + R * D + R + r) * 4, l);
+          }
         }
       }
     }
     if (!whole) {
-      const int64_t first = ((u0 + 1) * W - 1) / U, last = ((u0 + it.units) * W - 1) / U;   // runs with a part
-      unsigned* arrived = a.arrivals + (int64_t)entry * heads + h;
+      const int first = runs.of(u0), last = runs.of(u0 + it.units - 1);   // the runs with a part
       wait_mem();
       __syncthreads();
       if (tid == 0) {
+        unsigned* arrived = a.arrivals + (int64_t)entry * heads + h;
         const unsigned was = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         is_last = was == (unsigned)(last - first);
         if (is_last) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       __syncthreads();
       if (uni(is_last)) {
-        // The first run's part is its second one unless the item starts that run.
-        const int64_t side0 = first * U / W < u0 ? 1 : 0;
-        for (int rt = 0; rt < RT; ++rt) {
-          const int row16 = tid >> 4, share = tid & 15;
-          float m = -INFINITY, l = 0.0f, v[S];
+        // The first run's part is its second one unless the item starts that
+        // run.  A thread joins 4 numbers of a row; the loads of kAhead parts
+        // are in flight together.
+        constexpr int kAhead = 8, kPerRow = D / 4;
+        const int side0 = runs.start(first) < u0 ? 1 : 0;
+        for (int r = tid / kPerRow; r < used; r += kThreads / kPerRow) {
+          const int d = tid % kPerRow * 4;
+          float m = -INFINITY, l = 0.0f;
+          f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int w = first; w <= last; w += kAhead) {
+            float pm[kAhead], pl[kAhead];
+            f32x4 pv[kAhead];
 #pragma unroll
-          for (int d = 0; d < S; ++d) v[d] = 0.0f;
-#pragma unroll 2
-          for (int64_t w = first; w <= last; ++w) {
-            const float* q = a.parts + (2 * w + (w == first ? side0 : 0)) * kPart;
-            const float pm = ld_dev_f(q + R * D + rt * 16 + row16), pl = ld_dev_f(q + R * D + R + rt * 16 + row16);
-            float pv[S];
+            for (int j = 0; j < kAhead; ++j) {
+              const int x = min(w + j, last), at = (2 * x + (x == first ? side0 : 0)) * kPart;
+              pm[j] = ld_part1(parts, (at + R * D + r) * 4);
+              pl[j] = ld_part1(parts, (at + R * D + R + r) * 4);
+              pv[j] = ld_part(parts, (at + r * D + d) * 4);
+            }
+            float top = m;
 #pragma unroll
-            for (int d = 0; d < S; ++d) pv[d] = ld_dev_f(q + (rt * 16 + row16) * D + share * S + d);
-            const float top = fmaxf(m, pm), safe = top == -INFINITY ? 0.0f : top;
-            const float f0 = exp2_fast(m - safe), f1 = exp2_fast(pm - safe);
+            for (int j = 0; j < kAhead; ++j) top = fmaxf(top, pm[j]);
+            const float safe = top == -INFINITY ? 0.0f : top, f0 = exp2_fast(m - safe);
             m = top;
-            l = l * f0 + pl * f1;
+            l *= f0;
+            v *= f0;
 #pragma unroll
-            for (int d = 0; d < S; ++d) v[d] = v[d] * f0 + pv[d] * f1;
+            for (int j = 0; j < kAhead; ++j) {
+              if (w + j <= last) {
+                const float f = exp2_fast(pm[j] - safe);
+                l += pl[j] * f;
+                v += pv[j] * f;
+              }
+            }
           }
-          const int row = rg * R + rt * 16 + row16, token = row / a.group, head = h * a.group + row % a.group;
-          if (token < it.s.count) {
-            const int64_t at = ((int64_t)b * a.c.n + token) * a.heads_q + head;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-            for (int d = 0; d < S; ++d) v[d] *= inv;
-            store_row<D, DT>(a.out, at * D + share * S, v);
-            if (a.lse && share == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-          }
+          const int64_t at = place_of(r);
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+          store_numbers<D, DT, 4>(a.out, at * D + d, o);
+          if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
       }
     }
@@ -671,6 +776,7 @@ extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int 
   const hipStream_t st = static_cast<hipStream_t>(stream);
   // No more work-groups than units the call can have at most.
   const int64_t most = (int64_t)B * a.groups * cache->heads * (((int64_t)cache->table_len * cache->page + kUnitKeys - 1) / kUnitKeys + 1);
+  if (most > INT_MAX) return SPEC_EINVAL;
 #define SV_LAUNCH(D, DT, RT)                                                                                       \
   if (cache->dim == D && dt == (int)DT && rt == RT) {                                                              \
     const int grid = (int)(most < grid_for(D, DT, RT) ? most : grid_for(D, DT, RT));                               \
