@@ -31,13 +31,16 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 32;               // keys per wave and step
 constexpr int kUnitKeys = kWaves * kBlock;   // keys per work-group and step
+constexpr int kItemUnits = 2;
 constexpr int kCUs = 256;                // MI355X
+constexpr int kSpans = 512;              // sequences whose positions a work-group keeps in shared memory
 
 struct AttentionArgs {
   CacheView c;
   const void* q;
   int64_t q_stride;
   int heads_q, group;   // query heads, query heads per key/value head
+  unsigned by_group;    // ceil(2^32 / group): row / group = the upper half of row * by_group
   int groups;           // row groups per sequence and key/value head
   float c2;             // |scale| log2(e)
   int flip, zero;       // scale < 0; scale == 0 (or too small for a float): the queries are taken as 0
@@ -54,8 +57,8 @@ constexpr int kTerms = DT == kBF16 ? 1 : 3;   // bfloat16 parts that a query or 
 
 // Waves per SIMD the registers of a variant leave room for.
 constexpr int waves_for(int D, int dt, int rt) {
-  const int regs = rt * (D / 4 + (dt == kBF16 ? 12 : 20)) + D / 4 + 64;
-  return regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+  const int regs = rt * (D / 4 + (dt == kBF16 ? 12 : 16)) + D / 4 + 88;
+  return regs <= 164 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
 }
 // Row tiles of a group, at most.
 constexpr int max_tiles(int D, int dt) { return dt == kBF16 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2); }
@@ -72,14 +75,22 @@ struct Item {
   int tok0, tok1;   // its first and last token
   int lo, hi;       // positions, lo on a block's border
   int units;        // 0: no row of the group is in use
+  // What the item weighs when the work is divided: an item costs about as
+  // much time as kItemUnits units besides its keys (queries in, waves joined,
+  // results out).
+  __device__ __forceinline__ int weight() const { return units > 0 ? units + kItemUnits : 0; }
 };
 
-__device__ __forceinline__ Item item_of(const AttentionArgs& a, int b, int rg, int rows) {
+__device__ __forceinline__ int token_of(const AttentionArgs& a, int row) {
+  return a.group == 1 ? row : (int)__umulhi((unsigned)row, a.by_group);
+}
+
+__device__ __forceinline__ Item item_of(const AttentionArgs& a, Span span, int rg, int rows) {
   Item it;
-  it.s = span_of(a.c, b);
+  it.s = span;
   const int used = it.s.count < 0 ? a.c.n : it.s.count;
-  it.tok0 = rg * rows / a.group;
-  it.tok1 = min((rg * rows + rows - 1) / a.group, used - 1);
+  it.tok0 = token_of(a, rg * rows);
+  it.tok1 = min(token_of(a, rg * rows + rows - 1), used - 1);
   if (it.tok0 >= used) {
     it.units = 0;
     return it;
@@ -105,12 +116,12 @@ struct Half {   // of the keys, or of the values
 template <int D>
 __device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t rs, int voff, int soff, uint32_t (&w)[D / 32]) {
   if constexpr (D == 64) {
-    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0);
+    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 2);
     w[0] = t.x; w[1] = t.y;
   } else {
 #pragma unroll
     for (int x = 0; x < D / 128; ++x) {
-      const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + 16 * x, soff, 0);
+      const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + 16 * x, soff, 2);
       w[4 * x] = t.x; w[4 * x + 1] = t.y; w[4 * x + 2] = t.z; w[4 * x + 3] = t.w;
     }
   }
@@ -201,15 +212,19 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[TERMS]
   }
 }
 
+// Powers of two that a weight may pass 1 by before the row's reference moves:
+// float32 and bfloat16 lose nothing to it, and T keys of it are far from their largest numbers.
+constexpr float kSlack = 16.0f;
+
 template <int D, int DT, int RT>
 struct State {   // one wave's running result; a lane holds query (lane & 15) of each tile
   f32x4 o[RT][D / 16];
-  float m[RT], l[RT];   // maximum (base 2), and the sum over the lane's own keys
+  float m[RT], l[RT];   // reference (base 2; -inf before the first key), and the sum over the lane's own keys
 };
 
 // Whether a group's queries are kept in shared memory (else in registers).
 template <int DT, int RT>
-constexpr bool kQueriesShared = RT * kTerms<DT> > 1;
+constexpr bool kQueriesShared = true;
 
 template <int D, int DT, int RT>
 struct Rows {   // the group's queries
@@ -285,26 +300,32 @@ __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& 
   for (int rt = 0; rt < RT; ++rt) {
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s[rt][e >> 2][e & 3] * a.c2;
+    for (int e = 0; e < 8; ++e) x[e] = s[rt][e >> 2][e & 3];
     if (masked || nan_keys) {
-      const int at = it.s.pos + rows.token[rt];
-      const bool used = rows.token[rt] < it.s.count;
+      int at = it.s.pos + rows.token[rt], g4 = 4 * g;
+      asm volatile("" : "+v"(at), "+v"(g4));   // computed here, not kept over the loop
+      const int token = at - it.s.pos;
+      const bool used = token < it.s.count;
       const int last = !used ? -1 : a.mask ? it.s.pos - 1 : at;
-      const uint64_t bits = (a.mask && used) ? a.mask[(int64_t)b * a.c.n + rows.token[rt]] : 0;
+      const uint64_t bits = (a.mask && used) ? a.mask[(int64_t)b * a.c.n + token] : 0;
       const int first = a.window > 0 ? at - a.window + 1 : 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int in = 16 * (e >> 2) + 4 * g + (e & 3), key = p + in, j = key - it.s.pos;
+        const int in = 16 * (e >> 2) + g4 + (e & 3), key = p + in, j = key - it.s.pos;
         const bool sees = key >= first && (key <= last || (j >= 0 && j < it.s.count && (bits >> j & 1)));
         if (nan_keys >> in & 1) x[e] = __uint_as_float(0x7FC00000u);
         x[e] = sees ? x[e] : -INFINITY;
       }
     }
-    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    const auto max2 = [](float u, float v) { return fmaxf(u, v); };
-    top = swap_combine<16>(top, max2);
-    top = swap_combine<32>(top, max2);
-    if (__any(top > st.m[rt])) {
+    // The reference m only has to keep 2^(x - m) in range, so it moves when a
+    // score passes it by more than kSlack: most blocks need neither the
+    // exchange between lanes nor the rescaling.  (med3 with the largest float
+    // is a maximum that does not quiet NaNs first.)
+    const auto max2 = [](float u, float v) { return __builtin_amdgcn_fmed3f(u, v, FLT_MAX); };
+    float top = max2(max2(max2(x[0], x[1]), max2(x[2], x[3])), max2(max2(x[4], x[5]), max2(x[6], x[7])));
+    if (__any(top * a.c2 > st.m[rt] + kSlack)) {
+      const auto maxf = [](float u, float v) { return fmaxf(u, v); };
+      top = swap_combine<32>(swap_combine<16>(top, maxf), maxf) * a.c2;
       const float m = fmaxf(st.m[rt], top);
       const float alpha = exp2_fast(st.m[rt] - (m == -INFINITY ? 0.0f : m));
       st.l[rt] *= alpha;
@@ -314,7 +335,7 @@ __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& 
     }
     const float safe = st.m[rt] == -INFINITY ? 0.0f : st.m[rt];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = exp2_fast(x[e] - safe);
+    for (int e = 0; e < 8; ++e) x[e] = exp2_fast(fmaf(x[e], a.c2, -safe));
     st.l[rt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     split8<kTerms<DT>>(x, w[rt]);
   }
@@ -415,22 +436,31 @@ __device__ __forceinline__ int scalar_at(const int32_t* p, int at) {
 // workspace, and the last to arrive joins the parts in order.  A run has at
 // most two such parts, its first and its last.
 template <int D, int DT, int RT>
-__global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kernel(AttentionArgs) {
+  const AttentionArgs& a = kernel_arg0<AttentionArgs>();
   constexpr int R = 16 * RT, S = D / 16, kPart = R * (D + 2), T = kTerms<DT>;
   constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = kQueriesShared<DT, RT> ? R * D * 2 * T : 0;
   __shared__ __align__(16) char space[kSums > kQ ? kSums : kQ];   // the queries, then the waves' results
   __shared__ float tops[kWaves][R], totals[kWaves][R];
   __shared__ int scan[kWaves], found_start, found_entry, is_last;
+  __shared__ Span spans[kSpans];
   float (&sums)[kWaves][16][D + 4] = *reinterpret_cast<float (*)[kWaves][16][D + 4]>(space);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int heads = a.c.heads, entries = a.c.B * a.groups;
 
-  // Units of one head before this thread's entries, and in all (the host keeps them within 31 bits).
+  for (int b = tid; b < min(a.c.B, kSpans); b += kThreads) spans[b] = span_of(a.c, b);
+  __syncthreads();
+  const auto span_at = [&](int b) { return b < kSpans ? spans[b] : span_of(a.c, b); };
+  const auto weight_at = [&](int entry) {
+    const int b = entry / a.groups;
+    return item_of(a, span_at(b), entry - b * a.groups, R).weight();
+  };
+  // Weight of one head before this thread's entries, and in all (the host keeps them within 31 bits).
   const int per = (entries + kThreads - 1) / kThreads;
   const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
   int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += item_of(a, e / a.groups, e % a.groups, R).units;
+  for (int e = e0; e < e1; ++e) mine += weight_at(e);
   int before = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -454,7 +484,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   if (before * heads <= u && u < (before + mine) * heads) {
     int start = before * heads;
     for (int e = e0; e < e1; ++e) {
-      const int units = item_of(a, e / a.groups, e % a.groups, R).units * heads;
+      const int units = weight_at(e) * heads;
       if (u < start + units) {
         found_entry = e;
         found_start = start;
@@ -469,21 +499,23 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   const __amdgpu_buffer_rsrc_t parts = chunk_rsrc(a.parts, (int)(2 * gridDim.x * kPart * sizeof(float)));
 
   while (u < u1) {
-    const int b = entry / a.groups, rg = entry % a.groups;
-    const Item it = item_of(a, b, rg, R);
-    if (u >= entry_start + it.units * heads) {
-      entry_start += it.units * heads;
+    const int b = entry / a.groups, rg = entry - b * a.groups;
+    const Span span = span_at(b);
+    const Item it = item_of(a, {uni(span.pos), uni(span.count)}, rg, R);
+    const int weight = it.weight();
+    if (u >= entry_start + weight * heads) {
+      entry_start += weight * heads;
       ++entry;
       continue;
     }
-    const int h = (u - entry_start) / it.units;
-    const int u0 = entry_start + h * it.units;   // the item's first unit
-    const int k0 = u - u0, k1 = min(u1 - u0, it.units);
+    const int h = (u - entry_start) / weight;
+    const int u0 = entry_start + h * weight;   // the item's first unit; its last kItemUnits have no keys
+    const int k0 = u - u0, k1 = min(u1 - u0, weight);
     const int row0 = rg * R;
     // Rows in use; all n tokens' after a range error.
     const int used = min(R, (it.s.count < 0 ? a.c.n : it.s.count) * a.group - row0);
     const auto place_of = [&](int r) {   // row r of the group in q and out, in rows of D
-      const int row = row0 + r, token = row / a.group;
+      const int row = row0 + r, token = token_of(a, row);
       return ((int64_t)b * a.c.n + token) * a.heads_q + h * a.group + (row - token * a.group);
     };
 
@@ -491,13 +523,34 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       float nan[S];
 #pragma unroll
       for (int d = 0; d < S; ++d) nan[d] = __uint_as_float(0x7FC00000u);
-      for (int r = tid >> 4; r < used; r += 16) {
+      for (int r = tid >> 4; r < used && k0 == 0; r += 16) {
         const int64_t at = place_of(r);
         store_numbers<D, DT, S>(a.out, at * D + (tid & 15) * S, nan);
         if (a.lse && (tid & 15) == 0) a.lse[at] = nan[0];
       }
-      u += 1;
+      u = u0 + k1;
       continue;
+    }
+
+    // The wave's blocks p = lo + 128 k + 32 wave below hi.  The next block is
+    // loaded when this one's keys have been used, its page number a block
+    // earlier; the first one, before the queries.
+    const int32_t* table = a.c.table + (int64_t)b * a.c.table_len;
+    const int p1 = min(it.hi, it.lo + kUnitKeys * k1), P = 1 << a.c.page_log2;
+    int p = it.lo + kUnitKeys * k0 + kBlock * wave;
+    const auto page_at = [&](int pos) {   // positions behind the run read the run's last page
+      const int page = scalar_at(table, min(pos, p1 - 1) >> a.c.page_log2);
+      return (page >= 0 && page < a.c.pages) ? page : -1;
+    };
+    Half<D> k, v[2];
+    int page = -1, next = -1;
+    __amdgpu_buffer_rsrc_t rec;
+    if (p < p1) {
+      page = page_at(p);
+      next = page_at(p + kUnitKeys);
+      rec = record_rsrc<D>(a, page, h);
+      load_keys<D>(rec, p & (P - 1), places, k);
+      load_values<D>(rec, p & (P - 1), places, v[0]);
     }
 
     Rows<D, DT, RT> rows;
@@ -505,7 +558,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     rows.shared = reinterpret_cast<const u32x4*>(space);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = row0 + rt * 16 + i, token = row / a.group, head = h * a.group + (row - token * a.group);
+      const int row = row0 + rt * 16 + i, token = token_of(a, row), head = h * a.group + (row - token * a.group);
       rows.token[rt] = token;
       const bool live = token < it.s.count && !a.zero;
       const int64_t at = ((int64_t)b * a.c.n + token) * a.q_stride + (int64_t)head * D + g * (D / 4);
@@ -535,55 +588,46 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     }
     if constexpr (kQueriesShared<DT, RT>) __syncthreads();
 
-    // The wave's blocks p = lo + 128 k + 32 wave below hi.  The next block's
-    // keys are loaded when this one's have been used, and so its values.
-    const int32_t* table = a.c.table + (int64_t)b * a.c.table_len;
-    const int p1 = min(it.hi, it.lo + kUnitKeys * k1), P = 1 << a.c.page_log2;
-    int p = it.lo + kUnitKeys * k0 + kBlock * wave;
-    const auto page_at = [&](int pos) {   // positions behind the run read the run's last page
-      const int page = scalar_at(table, min(pos, p1 - 1) >> a.c.page_log2);
-      return (page >= 0 && page < a.c.pages) ? page : -1;
-    };
     if (p < p1) {
-      Half<D> k, v;
-      int page = page_at(p);
-      __amdgpu_buffer_rsrc_t rec = record_rsrc<D>(a, page, h);
-      load_keys<D>(rec, p & (P - 1), places, k);
-      load_values<D>(rec, p & (P - 1), places, v);
-      int next = page_at(p + kUnitKeys);
-      for (;;) {
+      // One block, values in v0; the next one's go to v1.  False after the last.
+      const auto step = [&](Half<D>& v0, Half<D>& v1) __attribute__((always_inline)) {
         const int pn = p + kUnitKeys;
         const bool more = pn < p1;
         f32x4 s[RT][2];
         bf16x8 w[RT][T];
         if (page < 0) {
           k.sc[0] = k.sc[1] = D == 256 ? 0xFFFFu : 0xFFu;
-          v.sc[0] = v.sc[1] = 0xFFFFFFFFu;
+          v0.sc[0] = v0.sc[1] = 0xFFFFFFFFu;
         }
         const bool masked = p + kBlock - 1 > (a.mask ? it.s.pos - 1 : it.s.pos + it.tok0) ||
                             (a.window > 0 && p <= it.s.pos + it.tok1 - a.window);
         score_block<D, DT, RT>(k, rows, lane, s);
         const uint32_t ks0 = k.sc[0], ks1 = k.sc[1];
+        __builtin_amdgcn_sched_barrier(0);
         rec = record_rsrc<D>(a, more ? next : -1, h);
         load_keys<D>(rec, pn & (P - 1), places, k);
+        load_values<D>(rec, pn & (P - 1), places, v1);
+        page = next;
+        next = page_at(pn + kUnitKeys);
         uint32_t nan_keys = 0;
-        if (__any((int)(has_ff(ks0) | has_ff(ks1) | has_ff(v.sc[0]) | has_ff(v.sc[1]))))
-          nan_keys = find_nan_keys<D>(ks0, ks1, v.sc);
+        if (__any((int)(has_ff(ks0) | has_ff(ks1) | has_ff(v0.sc[0]) | has_ff(v0.sc[1]))))
+          nan_keys = find_nan_keys<D>(ks0, ks1, v0.sc);
         if (masked) {
           // Places behind the last token hold anything: no scale of theirs may give an infinity.
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            uint32_t& x = v.sc[e >> 2];
+            uint32_t& x = v0.sc[e >> 2];
             if ((x >> (8 * (e & 3)) & 255) > 252) x = (x & ~(255u << (8 * (e & 3)))) | 127u << (8 * (e & 3));
           }
         }
         weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, rows, s, st, w);
-        gather_block<D, DT, RT>(v, w, st);
-        if (!more) break;
-        load_values<D>(rec, pn & (P - 1), places, v);
+        __builtin_amdgcn_sched_barrier(0);
+        gather_block<D, DT, RT>(v0, w, st);
+        __builtin_amdgcn_sched_barrier(0);
         p = pn;
-        page = next;
-        next = page_at(p + kUnitKeys);
+        return more;
+      };
+      while (step(v[0], v[1]) && step(v[1], v[0])) {
       }
     }
 
@@ -598,7 +642,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       }
     }
     __syncthreads();
-    const bool whole = k0 == 0 && k1 == it.units;
+    const bool whole = k0 == 0 && k1 == weight;
     const int part = (2 * run + (u == u_begin ? 0 : 1)) * kPart;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -643,7 +687,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       }
     }
     if (!whole) {
-      const int first = runs.of(u0), last = runs.of(u0 + it.units - 1);   // the runs with a part
+      const int first = runs.of(u0), last = runs.of(u0 + weight - 1);   // the runs with a part
       wait_mem();
       __syncthreads();
       if (tid == 0) {
@@ -682,7 +726,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
             v *= f0;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-              if (w + j <= last) {
+              if (w + j <= last && pm[j] != -INFINITY) {
                 const float f = exp2_fast(pm[j] - safe);
                 l += pl[j] * f;
                 v += pv[j] * f;
@@ -708,6 +752,8 @@ int check_attention(int B, int n, int heads_q, int heads, int dim) {
   if (B > 0 && heads_q > (((int64_t)1 << 34) / dim) / ((int64_t)B * n)) return SPEC_EINVAL;
   const int64_t groups = ((int64_t)n * (heads_q / heads) + 15) / 16;
   if (B > 0 && groups * heads > ((int64_t)1 << 24) / B) return SPEC_EINVAL;
+  // row / group by a multiplication needs rows * group < 2^32 (with room for a last group's rows)
+  if (((int64_t)n * (heads_q / heads) + 64) * (heads_q / heads) >= ((int64_t)1 << 32)) return SPEC_EINVAL;
   return SPEC_OK;
 }
 
@@ -770,12 +816,13 @@ extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int 
   a.arrivals = static_cast<unsigned*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + arrival_bytes(B, n, heads_q, cache->heads));
   const int64_t rows = (int64_t)n * a.group;
+  a.by_group = (unsigned)((((uint64_t)1 << 32) + a.group - 1) / a.group);
   const int dt = dtype == SPEC_BF16 ? (int)kBF16 : (int)kF32, rt = tiles_for(cache->dim, dt, rows);
   a.groups = (int)((rows + 16 * rt - 1) / (16 * rt));
   (void)hipGetLastError();
   const hipStream_t st = static_cast<hipStream_t>(stream);
   // No more work-groups than units the call can have at most.
-  const int64_t most = (int64_t)B * a.groups * cache->heads * (((int64_t)cache->table_len * cache->page + kUnitKeys - 1) / kUnitKeys + 1);
+  const int64_t most = (int64_t)B * a.groups * cache->heads * (((int64_t)cache->table_len * cache->page + kUnitKeys - 1) / kUnitKeys + 1 + kItemUnits);
   if (most > INT_MAX) return SPEC_EINVAL;
 #define SV_LAUNCH(D, DT, RT)                                                                                       \
   if (cache->dim == D && dt == (int)DT && rt == RT) {                                                              \
