@@ -57,8 +57,8 @@ constexpr int kTerms = DT == kBF16 ? 1 : 3;   // bfloat16 parts that a query or 
 
 // Waves per SIMD the registers of a variant leave room for.
 constexpr int waves_for(int D, int dt, int rt) {
-  const int regs = rt * (D / 4 + (dt == kBF16 ? 12 : 16)) + D / 4 + 88;
-  return regs <= 164 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+  const int regs = rt * (D / 4 + 16) + D / 2 + 36;
+  return regs <= 128 ? 4 : regs <= 168 ? 3 : 2;
 }
 // Row tiles of a group, at most.
 constexpr int max_tiles(int D, int dt) { return dt == kBF16 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2); }
