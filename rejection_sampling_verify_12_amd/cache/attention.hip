@@ -31,7 +31,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 32;               // keys per wave and step
 constexpr int kUnitKeys = kWaves * kBlock;   // keys per work-group and step
-constexpr int kItemUnits = 2;
+constexpr int kItemUnits = 4;
 constexpr int kCUs = 256;                // MI355X
 constexpr int kSpans = 512;              // sequences whose positions a work-group keeps in shared memory
 
@@ -106,7 +106,10 @@ __device__ __forceinline__ Item item_of(const AttentionArgs& a, Span span, int r
   return it;
 }
 
-// A lane's share of a block of 32 keys: codes and scales of 2 tiles of 16 keys.
+// A lane's share of a block of 32 keys: codes and scales of 2 tiles of 16
+// keys.  Scales are loaded as the 4 bytes that hold the lane's and cut out
+// where they are used: a load of 1 or 2 bytes is widened by an instruction
+// that waits for it, right behind the load.
 template <int D>
 struct Half {   // of the keys, or of the values
   uint32_t w[2][D / 32];
@@ -131,21 +134,22 @@ __device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t rs, int voff, 
 template <int D>
 struct Places {
   int k, v, ks, vs;
+  int kbit;   // where the lane's key scales (8 bits, 16 at dim 256) start in their 32
   __device__ __forceinline__ Places(int P, int lane) {
     using F = Format<D>;
     const int i = lane & 15, g = lane >> 4;
     k = i * F::kRow + g * (D / 8);
     v = F::values(P, 0, 0) + g * (2 * D) + i * (D / 8);
-    ks = F::key_scales(P, 0) + i * F::kBlocks + (D == 256 ? 2 * g : D == 128 ? g : g >> 1);
+    const int scale = i * F::kBlocks + (D == 256 ? 2 * g : D == 128 ? g : g >> 1);
+    ks = F::key_scales(P, 0) + (scale & ~3);
+    kbit = 8 * (scale & 3);
     vs = F::value_scale(P, 0, 0) + i * (D / 16) / 32 * 16 + 4 * g;
   }
 };
 
-// The record of one page and head, or no bytes for a page outside the pool.
-template <int D>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t record_rsrc(const AttentionArgs& a, int page, int h) {
-  const int bytes = Format<D>::record(1 << a.c.page_log2);
-  return chunk_rsrc(a.c.data + ((int64_t)max(page, 0) * a.c.heads + h) * bytes, page < 0 ? 0 : bytes);
+// The record of one page and one head of it, or no bytes for a page outside the pool.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t record_rsrc(const uint8_t* head, int64_t page_bytes, int page, int bytes) {
+  return chunk_rsrc(head + max(page, 0) * page_bytes, page < 0 ? 0 : bytes);
 }
 template <int D>
 __device__ __forceinline__ void load_keys(__amdgpu_buffer_rsrc_t rs, int r, const Places<D>& at, Half<D>& x) {
@@ -153,11 +157,7 @@ __device__ __forceinline__ void load_keys(__amdgpu_buffer_rsrc_t rs, int r, cons
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     load_words<D>(rs, at.k + 16 * t * F::kRow, r * F::kRow, x.w[t]);
-    if constexpr (D == 256) {
-      x.sc[t] = __builtin_amdgcn_raw_buffer_load_b16(rs, at.ks + 16 * t * F::kBlocks, r * F::kBlocks, 0);
-    } else {
-      x.sc[t] = __builtin_amdgcn_raw_buffer_load_b8(rs, at.ks + 16 * t * F::kBlocks, r * F::kBlocks, 0);
-    }
+    x.sc[t] = __builtin_amdgcn_raw_buffer_load_b32(rs, at.ks + 16 * t * F::kBlocks, r * F::kBlocks, 0);
   }
 }
 template <int D>
@@ -171,6 +171,8 @@ __device__ __forceinline__ void load_values(__amdgpu_buffer_rsrc_t rs, int r, co
   }
 }
 
+// The upper bits of bytes from 192 on: scales of 2^65 and NaN blocks, told apart by find_nan_keys.
+__device__ __forceinline__ uint32_t suspect(uint32_t w) { return w & (w << 1); }
 // Some byte of w is 255.
 __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
@@ -215,11 +217,12 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[TERMS]
 // Powers of two that a weight may pass 1 by before the row's reference moves:
 // float32 and bfloat16 lose nothing to it, and T keys of it are far from their largest numbers.
 constexpr float kSlack = 16.0f;
+constexpr float kNone = -FLT_MAX;
 
 template <int D, int DT, int RT>
 struct State {   // one wave's running result; a lane holds query (lane & 15) of each tile
   f32x4 o[RT][D / 16];
-  float m[RT], l[RT];   // reference (base 2; -inf before the first key), and the sum over the lane's own keys
+  float m[RT], l[RT];   // reference (base 2; kNone before the first key), and the sum over the lane's own keys
 };
 
 // Whether a group's queries are kept in shared memory (else in registers).
@@ -236,7 +239,7 @@ struct Rows {   // the group's queries
 // Scores of a block: rows = keys, columns = queries.  rt's tile t holds keys
 // 16 t + 4 (lane / 16) + 0 .. 3 of query lane % 16.
 template <int D, int DT, int RT>
-__device__ __forceinline__ void score_block(const Half<D>& x, const Rows<D, DT, RT>& rows, int lane, f32x4 (&s)[RT][2]) {
+__device__ __forceinline__ void score_block(const Half<D>& x, const uint32_t (&ks)[2], const Rows<D, DT, RT>& rows, int lane, f32x4 (&s)[RT][2]) {
   constexpr int T = kTerms<DT>;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -245,7 +248,7 @@ __device__ __forceinline__ void score_block(const Half<D>& x, const Rows<D, DT, 
     bf16x8 k[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const float sc = scale_of(D == 256 ? (c < 4 ? x.sc[t] & 255 : x.sc[t] >> 8) : x.sc[t]);
+      const float sc = scale_of(D == 256 ? (c < 4 ? ks[t] & 255 : ks[t] >> 8) : ks[t]);
       const uint32_t w = x.w[t][c];
       k[t] = as_bf16x8(cvt_pair(w, sc, 0), cvt_pair(w, sc, 1), cvt_pair(w, sc, 2), cvt_pair(w, sc, 3));
     }
@@ -293,7 +296,7 @@ __device__ __forceinline__ uint32_t find_nan_keys(uint32_t k0, uint32_t k1, uint
 // Weights of a block and the running maximum and sum.  `masked`: some row does not see some key.
 template <int D, int DT, int RT>
 __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& it, int b, int p, int lane, bool masked,
-                                            uint32_t nan_keys, const Rows<D, DT, RT>& rows, f32x4 (&s)[RT][2],
+                                            uint32_t nan_keys, float c2, const Rows<D, DT, RT>& rows, f32x4 (&s)[RT][2],
                                             State<D, DT, RT>& st, bf16x8 (&w)[RT][kTerms<DT>]) {
   const int g = lane >> 4;
 #pragma unroll
@@ -319,23 +322,21 @@ __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& 
     }
     // The reference m only has to keep 2^(x - m) in range, so it moves when a
     // score passes it by more than kSlack: most blocks need neither the
-    // exchange between lanes nor the rescaling.  (med3 with the largest float
-    // is a maximum that does not quiet NaNs first.)
-    const auto max2 = [](float u, float v) { return __builtin_amdgcn_fmed3f(u, v, FLT_MAX); };
-    float top = max2(max2(max2(x[0], x[1]), max2(x[2], x[3])), max2(max2(x[4], x[5]), max2(x[6], x[7])));
-    if (__any(top * a.c2 > st.m[rt] + kSlack)) {
+    // exchange between lanes nor the rescaling.  (A NaN moves nothing: its own
+    // weight says NaN.)
+    const auto max2 = [](float u, float v) { return __builtin_elementwise_maximum(u, v); };
+    float top = max2(max2(max2(x[0], x[1]), x[2]), max2(max2(x[3], x[4]), max2(max2(x[5], x[6]), x[7])));
+    if (__any(top * c2 > st.m[rt] + kSlack)) {
       const auto maxf = [](float u, float v) { return fmaxf(u, v); };
-      top = swap_combine<32>(swap_combine<16>(top, maxf), maxf) * a.c2;
-      const float m = fmaxf(st.m[rt], top);
-      const float alpha = exp2_fast(st.m[rt] - (m == -INFINITY ? 0.0f : m));
+      top = swap_combine<32>(swap_combine<16>(top, maxf), maxf) * c2;
+      const float m = fmaxf(st.m[rt], top), alpha = exp2_fast(st.m[rt] - m);
       st.l[rt] *= alpha;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) st.o[rt][d] *= alpha;
       st.m[rt] = m;
     }
-    const float safe = st.m[rt] == -INFINITY ? 0.0f : st.m[rt];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = exp2_fast(fmaf(x[e], a.c2, -safe));
+    for (int e = 0; e < 8; ++e) x[e] = exp2_fast(fmaf(x[e], c2, -st.m[rt]));
     st.l[rt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     split8<kTerms<DT>>(x, w[rt]);
   }
@@ -348,7 +349,7 @@ __device__ __forceinline__ void gather_block(const Half<D>& x, const bf16x8 (&w)
   constexpr int T = kTerms<DT>;
   float sc[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sc[e] = scale_of(x.sc[e >> 2] >> (8 * (e & 3)) & 255);
+  for (int e = 0; e < 8; ++e) sc[e] = scale_of(__builtin_amdgcn_ubfe(x.sc[e >> 2], 8 * (e & 3), 8));
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) {
     uint32_t y[8];
@@ -423,6 +424,13 @@ __device__ __forceinline__ float ld_part1(__amdgpu_buffer_rsrc_t rs, int byte) {
 }
 __device__ __forceinline__ void st_part1(__amdgpu_buffer_rsrc_t rs, int byte, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, byte, 0, kDeviceScope);
+}
+
+// A scalar that the loop keeps, rather than loading it from the arguments for each block.
+template <class V>
+__device__ __forceinline__ V pin(V x) {
+  asm volatile("" : "+s"(x));
+  return x;
 }
 
 // A table entry through the scalar cache: the address is the wave's.
@@ -536,11 +544,18 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     // loaded when this one's keys have been used, its page number a block
     // earlier; the first one, before the queries.
     const int32_t* table = a.c.table + (int64_t)b * a.c.table_len;
-    const int p1 = min(it.hi, it.lo + kUnitKeys * k1), P = 1 << a.c.page_log2;
+    const int log2 = pin(a.c.page_log2), P = 1 << log2, record = Format<D>::record(P), pages = pin(a.c.pages);
+    const uint8_t* head = pin(a.c.data + (int64_t)h * record);
+    const int64_t page_bytes = (int64_t)heads * record;
+    const float c2 = pin(a.c2);
+    const int p1 = min(it.hi, it.lo + kUnitKeys * k1);
     int p = it.lo + kUnitKeys * k0 + kBlock * wave;
+    // Blocks from whole0 to whole1 are seen by every row as a whole.
+    const int whole0 = a.window > 0 ? it.s.pos + it.tok1 - a.window + 1 : 0;
+    const int whole1 = (a.mask ? it.s.pos - 1 : it.s.pos + it.tok0) - (kBlock - 1);
     const auto page_at = [&](int pos) {   // positions behind the run read the run's last page
-      const int page = scalar_at(table, min(pos, p1 - 1) >> a.c.page_log2);
-      return (page >= 0 && page < a.c.pages) ? page : -1;
+      const int page = scalar_at(table, min(pos, p1 - 1) >> log2);
+      return (page >= 0 && page < pages) ? page : -1;
     };
     Half<D> k, v[2];
     int page = -1, next = -1;
@@ -548,7 +563,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     if (p < p1) {
       page = page_at(p);
       next = page_at(p + kUnitKeys);
-      rec = record_rsrc<D>(a, page, h);
+      rec = record_rsrc(head, page_bytes, page, record);
       load_keys<D>(rec, p & (P - 1), places, k);
       load_values<D>(rec, p & (P - 1), places, v[0]);
     }
@@ -581,7 +596,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
           rows.q[c] = q[0];
         }
       }
-      st.m[rt] = -INFINITY;
+      st.m[rt] = kNone;
       st.l[rt] = 0.0f;
 #pragma unroll
       for (int d = 0; d < S; ++d) st.o[rt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -595,23 +610,25 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         const bool more = pn < p1;
         f32x4 s[RT][2];
         bf16x8 w[RT][T];
+        uint32_t ks[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) ks[t] = __builtin_amdgcn_ubfe(k.sc[t], places.kbit, D == 256 ? 16 : 8);
         if (page < 0) {
-          k.sc[0] = k.sc[1] = D == 256 ? 0xFFFFu : 0xFFu;
+          ks[0] = ks[1] = D == 256 ? 0xFFFFu : 0xFFu;
           v0.sc[0] = v0.sc[1] = 0xFFFFFFFFu;
         }
-        const bool masked = p + kBlock - 1 > (a.mask ? it.s.pos - 1 : it.s.pos + it.tok0) ||
-                            (a.window > 0 && p <= it.s.pos + it.tok1 - a.window);
-        score_block<D, DT, RT>(k, rows, lane, s);
-        const uint32_t ks0 = k.sc[0], ks1 = k.sc[1];
+        const bool masked = p < whole0 || p > whole1;
+        score_block<D, DT, RT>(k, ks, rows, lane, s);
         __builtin_amdgcn_sched_barrier(0);
-        rec = record_rsrc<D>(a, more ? next : -1, h);
+        rec = record_rsrc(head, page_bytes, more ? next : -1, record);
         load_keys<D>(rec, pn & (P - 1), places, k);
         load_values<D>(rec, pn & (P - 1), places, v1);
         page = next;
         next = page_at(pn + kUnitKeys);
         uint32_t nan_keys = 0;
-        if (__any((int)(has_ff(ks0) | has_ff(ks1) | has_ff(v0.sc[0]) | has_ff(v0.sc[1]))))
-          nan_keys = find_nan_keys<D>(ks0, ks1, v0.sc);
+        const uint32_t both = ks[0] | ks[1] << (D == 256 ? 16 : 8);
+        if (__any((int)((suspect(both) | suspect(v0.sc[0]) | suspect(v0.sc[1])) & 0x80808080u)))
+          nan_keys = find_nan_keys<D>(ks[0], ks[1], v0.sc);
         if (masked) {
           // Places behind the last token hold anything: no scale of theirs may give an infinity.
 #pragma unroll
@@ -620,7 +637,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
             if ((x >> (8 * (e & 3)) & 255) > 252) x = (x & ~(255u << (8 * (e & 3)))) | 127u << (8 * (e & 3));
           }
         }
-        weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, rows, s, st, w);
+        weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, c2, rows, s, st, w);
         __builtin_amdgcn_sched_barrier(0);
         gather_block<D, DT, RT>(v0, w, st);
         __builtin_amdgcn_sched_barrier(0);
@@ -651,7 +668,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         float m = tops[0][rt * 16 + i];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][rt * 16 + i]);
-        const float f = exp2_fast(st.m[rt] - (m == -INFINITY ? 0.0f : m));
+        const float f = exp2_fast(st.m[rt] - m);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -663,9 +680,8 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         float m = tops[0][r], l = 0.0f, v[S];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][r]);
-        const float safe = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) l += totals[w][r] * exp2_fast(tops[w][r] - safe);
+        for (int w = 0; w < kWaves; ++w) l += totals[w][r] * exp2_fast(tops[w][r] - m);
 #pragma unroll
         for (int d = 0; d < S; ++d)
           v[d] = (sums[0][row16][share * S + d] + sums[1][row16][share * S + d]) + (sums[2][row16][share * S + d] + sums[3][row16][share * S + d]);
@@ -705,7 +721,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         const int side0 = runs.start(first) < u0 ? 1 : 0;
         for (int r = tid / kPerRow; r < used; r += kThreads / kPerRow) {
           const int d = tid % kPerRow * 4;
-          float m = -INFINITY, l = 0.0f;
+          float m = kNone, l = 0.0f;
           f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int w = first; w <= last; w += kAhead) {
             float pm[kAhead], pl[kAhead];
@@ -720,14 +736,14 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
             float top = m;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) top = fmaxf(top, pm[j]);
-            const float safe = top == -INFINITY ? 0.0f : top, f0 = exp2_fast(m - safe);
+            const float f0 = exp2_fast(m - top);
             m = top;
             l *= f0;
             v *= f0;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-              if (w + j <= last && pm[j] != -INFINITY) {
-                const float f = exp2_fast(pm[j] - safe);
+              if (w + j <= last) {
+                const float f = exp2_fast(pm[j] - top);
                 l += pl[j] * f;
                 v += pv[j] * f;
               }
