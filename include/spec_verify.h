@@ -500,10 +500,10 @@ int spec_lds_atomic_probe(int pattern, int iters, uint64_t* sink, void* stream);
  *   (nullable).  Outputs must not overlap inputs.
  *   Scores, the softmax's maximum and sum and the output are held in 32 bits;
  *   bf16 calls round the weights to bf16 for the product with the values.
- *   The workspace must be zero-filled before its first use and is left
- *   ready for the next call, as spec_workspace_bytes() describes; a call's
- *   workspace serves every call with as many or fewer sequences, tokens and
- *   heads.  Results do not depend on which work-group finishes first.
+ *   The workspace (on a 16-byte boundary) may hold anything; calls that may
+ *   overlap need one each; it serves every call with as many or fewer
+ *   sequences, tokens and heads.  Results do not depend on which work-group
+ *   finishes first.
  */
 typedef struct spec_cache {
   void* data;

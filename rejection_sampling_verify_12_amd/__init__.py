@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import collections
 import ctypes
-import math
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -521,33 +520,35 @@ def spec_verify_predict(draft_logits, target_logits, draft_tokens, u_accept, u_s
     return out, pred
 
 
+# Bytes of one page and head by (page, dim): spec_cache_page_bytes for what the library supports.
+_PAGE_BYTES = {(page, dim): page * (dim + dim // 16) for page in (32, 64, 128, 256) for dim in (64, 128, 256)}
+
+
 class QuantCache:
     """A key/value cache in 4 bits (see spec_verify.h): ``data`` uint8
     [pages, heads, spec_cache_page_bytes(page, dim)], ``table`` int32 [B, table_len],
     the page of every ``page`` positions of each sequence.  The tensors are the
     caller's; entries of ``table`` may change between calls."""
 
-    __slots__ = ("data", "table", "page", "dim", "_c")
+    __slots__ = ("data", "table", "page", "dim", "heads", "B", "index", "_c", "_ref")
 
     def __init__(self, data, table, page: int, dim: int):
         import torch
-        nbytes = spec_cache_page_bytes(page, dim)
-        if not nbytes:
+        nbytes = _PAGE_BYTES.get((page, dim))
+        if nbytes is None:
             raise ValueError(f"page is 32, 64, 128 or 256 and dim 64, 128 or 256, got {page} and {dim}")
-        if data.dtype != torch.uint8 or data.dim() != 3 or data.shape[2] != nbytes:
-            raise ValueError(f"data is uint8 [pages, heads, {nbytes}], got {data.dtype} {tuple(data.shape)}")
-        if table.dtype != torch.int32 or table.dim() != 2:
-            raise ValueError(f"table is int32 [B, table_len], got {table.dtype} {tuple(table.shape)}")
+        shape, tshape = data.shape, table.shape
+        if data.dtype != torch.uint8 or len(shape) != 3 or shape[2] != nbytes:
+            raise ValueError(f"data is uint8 [pages, heads, {nbytes}], got {data.dtype} {tuple(shape)}")
+        if table.dtype != torch.int32 or len(tshape) != 2:
+            raise ValueError(f"table is int32 [B, table_len], got {table.dtype} {tuple(tshape)}")
         _check_dev(data, table)
-        if table.device != data.device:
-            raise ValueError("data and table must be on one device")
         self.data, self.table, self.page, self.dim = data, table, page, dim
-        self._c = SpecCache(data.data_ptr(), table.data_ptr(), data.shape[0], data.shape[1], page, dim,
-                            table.shape[1])
-
-    @property
-    def heads(self) -> int:
-        return self.data.shape[1]
+        self.heads, self.B, self.index = shape[1], tshape[0], data.get_device()
+        if table.get_device() != self.index:
+            raise ValueError("data and table must be on one device")
+        self._c = SpecCache(data.data_ptr(), table.data_ptr(), shape[0], shape[1], page, dim, tshape[1])
+        self._ref = ctypes.byref(self._c)
 
 
 def new_cache(pages: int, heads: int, dim: int, table, page: int = 64) -> QuantCache:
@@ -567,11 +568,12 @@ AttentionOut = collections.namedtuple("AttentionOut", "out lse")
 
 def _token_stride(name: str, x, heads: int, dim: int) -> int:
     """Elements between the tokens of x [B, n, heads, dim], whose heads lie side by side."""
-    if x.dim() != 4 or x.shape[2] != heads or x.shape[3] != dim:
-        raise ValueError(f"{name} is [B, n, {heads}, {dim}], got {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != dim:
+        raise ValueError(f"{name} is [B, n, {heads}, {dim}], got {tuple(shape)}")
     if x.is_contiguous():
         return heads * dim
-    B, n = x.shape[:2]
+    B, n = shape[:2]
     s = x.stride()
     if s[3] != 1 or (heads > 1 and s[2] != dim) or (B > 1 and n > 1 and s[0] != n * s[1]):
         raise ValueError(f"{name}: the numbers and heads of a token must lie side by side and the tokens of "
@@ -579,30 +581,41 @@ def _token_stride(name: str, x, heads: int, dim: int) -> int:
     return s[1] if n > 1 else s[0]
 
 
-def _check_cache_call(cache: QuantCache, B: int, n: int, ints, rest):
-    """Types, shapes and devices of a cache call's arrays: ``ints`` are int32 [B]."""
+def _per_sequence(cache: QuantCache, t):
+    """The address of an int32 [B] array of a cache call, or None."""
     import torch
-    dev = cache.data.device
-    if cache.table.shape[0] != B:
-        raise ValueError(f"the table has {cache.table.shape[0]} sequences, the call {B}")
-    for t in ints:
-        if t is not None:
-            if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B:
-                raise ValueError(f"length, count and status are int32 [{B}], got {t.dtype} {tuple(t.shape)}")
-            if t.device != dev or not t.is_contiguous():
-                raise ValueError("every tensor must be a contiguous tensor on the cache's device")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError("every tensor must be on the cache's device")
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != (cache.B,):
+        raise ValueError(f"length, count and status are int32 [{cache.B}], got {t.dtype} {tuple(t.shape)}")
+    return _on_device(cache, t)
 
 
-def _cache_launch(f, dev, stream, *args):
+def _on_device(cache: QuantCache, t):
+    """The address of a contiguous tensor on the cache's device."""
+    if t.get_device() != cache.index or not t.is_contiguous():
+        raise ValueError("every tensor must be a contiguous tensor on the cache's device")
+    return t.data_ptr()
+
+
+def _current_stream(index: int) -> int:
+    """The handle of the device's current stream (torch's own accessor for launchers where it has one: a
+    stream object costs as much as the rest of a small call's checks)."""
     import torch
-    if torch.cuda.current_device() == dev.index:
-        st = f(*args, _stream_handle(stream, dev))
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _cache_launch(f, cache: QuantCache, B: int, stream, *args):
+    import torch
+    if cache.B != B:
+        raise ValueError(f"the table has {cache.B} sequences, the call {B}")
+    dev = cache.index
+    if torch.cuda.current_device() == dev:
+        st = f(cache._ref, *args, _current_stream(dev) if stream is None else stream.cuda_stream)
     else:   # a launch goes to the current device
         with torch.cuda.device(dev):
-            st = f(*args, _stream_handle(stream, dev))
+            st = f(cache._ref, *args, _current_stream(dev) if stream is None else stream.cuda_stream)
     if st != SPEC_OK:
         raise SpecError(st)
 
@@ -612,14 +625,16 @@ def spec_cache_append(cache: QuantCache, k, v, length=None, lag: int = 0, count=
     into the cache, at positions length - lag onwards (see spec_verify.h).
     ``count`` int32 [B]: how many of the n tokens each sequence has.  Returns
     ``status`` (int32 [B], or None if none was given)."""
-    ks = _token_stride("k", k, cache.heads, cache.dim)
-    vs = _token_stride("v", v, cache.heads, cache.dim)
+    heads, dim = cache.heads, cache.dim
+    ks, vs = _token_stride("k", k, heads, dim), _token_stride("v", v, heads, dim)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must share shape and dtype")
+    if k.get_device() != cache.index or v.get_device() != cache.index:
+        raise ValueError("k and v must be on the cache's device")
     B, n = k.shape[:2]
-    _check_cache_call(cache, B, n, (length, count, status), (k, v))
-    _cache_launch(load_library().spec_cache_append, cache.data.device, stream, ctypes.byref(cache._c), k.data_ptr(),
-                  v.data_ptr(), _dtype_code(k), ks, vs, _ptr(length), lag, _ptr(count), B, n, _ptr(status))
+    _cache_launch((_lib or load_library()).spec_cache_append, cache, B, stream, k.data_ptr(), v.data_ptr(),
+                  _dtype_code(k), ks, vs, _per_sequence(cache, length), lag, _per_sequence(cache, count), B, n,
+                  _per_sequence(cache, status))
     return status
 
 
@@ -628,17 +643,17 @@ def spec_cache_read(cache: QuantCache, n: int, length=None, lag: int = 0, count=
     """The keys and values [B, n, heads, dim] that the cache holds at positions
     length - lag onwards, in ``dtype`` (float32, or bfloat16 by default) or into
     ``out`` (a CacheRows); rows behind ``count`` are left as they were."""
-    import torch
-    B, shape = cache.table.shape[0], (cache.table.shape[0], n, cache.heads, cache.dim)
+    B, shape = cache.B, (cache.B, n, cache.heads, cache.dim)
     if out is None:
+        import torch
         new = lambda: torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.data.device)
         out = CacheRows(new(), new())
-    if out.k.shape != shape or out.v.shape != shape or out.v.dtype != out.k.dtype or dtype not in (None, out.k.dtype):
+    k, v = out
+    if k.shape != shape or v.shape != shape or v.dtype != k.dtype or dtype not in (None, k.dtype):
         raise ValueError(f"out holds two tensors {shape} of one dtype")
-    _check_dev(out.k, out.v)
-    _check_cache_call(cache, B, n, (length, count, status), out)
-    _cache_launch(load_library().spec_cache_read, cache.data.device, stream, ctypes.byref(cache._c), _ptr(length), lag,
-                  _ptr(count), B, n, out.k.data_ptr(), out.v.data_ptr(), _dtype_code(out.k), _ptr(status))
+    _cache_launch((_lib or load_library()).spec_cache_read, cache, B, stream, _per_sequence(cache, length), lag,
+                  _per_sequence(cache, count), B, n, _on_device(cache, k), _on_device(cache, v), _dtype_code(k),
+                  _per_sequence(cache, status))
     return out
 
 
@@ -656,28 +671,30 @@ def spec_cache_attention(cache: QuantCache, q, length=None, lag: int = 0, count=
     AttentionOut to write, its lse None if not wanted; rows behind ``count`` are
     left as they were."""
     import torch
-    if q.dim() != 4:
-        raise ValueError(f"q is [B, n, heads_q, dim], got {tuple(q.shape)}")
-    B, n, heads_q, dim = q.shape
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q is [B, n, heads_q, dim], got {tuple(shape)}")
+    B, n, heads_q, dim = shape
     qs = _token_stride("q", q, heads_q, cache.dim)
-    dev = cache.data.device
+    if q.get_device() != cache.index:
+        raise ValueError("q must be on the cache's device")
     if out is None:
-        out = AttentionOut(torch.empty(q.shape, dtype=q.dtype, device=dev),
-                           torch.empty((B, n, heads_q), dtype=torch.float32, device=dev) if lse else None)
-    if out.out.shape != q.shape or out.out.dtype != q.dtype:
+        out = AttentionOut(torch.empty(shape, dtype=q.dtype, device=q.device),
+                           torch.empty((B, n, heads_q), dtype=torch.float32, device=q.device) if lse else None)
+    o, l = out
+    if o.shape != shape or o.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
-    if out.lse is not None and (out.lse.shape != q.shape[:3] or out.lse.dtype != torch.float32):
-        raise ValueError(f"lse is float32 {tuple(q.shape[:3])}")
-    if mask is not None and (mask.shape != q.shape[:2] or mask.dtype != torch.int64):
-        raise ValueError(f"mask is int64 {tuple(q.shape[:2])}")
+    if l is not None and (l.shape != shape[:3] or l.dtype != torch.float32):
+        raise ValueError(f"lse is float32 {tuple(shape[:3])}")
+    if mask is not None and (mask.shape != shape[:2] or mask.dtype != torch.int64):
+        raise ValueError(f"mask is int64 {tuple(shape[:2])}")
     if workspace is None:
-        workspace = new_workspace(spec_cache_attention_workspace_bytes(B, n, heads_q, cache.heads, cache.dim), dev)
-    _check_dev(out.out, out.lse, mask, workspace)
-    _check_cache_call(cache, B, n, (length, count), (q, out.out, out.lse, mask, workspace))
-    _cache_launch(load_library().spec_cache_attention, dev, stream, ctypes.byref(cache._c), q.data_ptr(),
-                  _dtype_code(q), qs, heads_q, _ptr(length), lag, _ptr(count), B, n,
-                  1.0 / math.sqrt(dim) if scale is None else scale, window, _ptr(mask), out.out.data_ptr(),
-                  _ptr(out.lse), workspace.data_ptr(), workspace.numel())
+        workspace = new_workspace(spec_cache_attention_workspace_bytes(B, n, heads_q, cache.heads, dim), q.device)
+    _cache_launch((_lib or load_library()).spec_cache_attention, cache, B, stream, q.data_ptr(), _dtype_code(q), qs,
+                  heads_q, _per_sequence(cache, length), lag, _per_sequence(cache, count), B, n,
+                  dim ** -0.5 if scale is None else scale, window, None if mask is None else _on_device(cache, mask),
+                  _on_device(cache, o), None if l is None else _on_device(cache, l), _on_device(cache, workspace),
+                  workspace.numel())
     return out
 
 

@@ -22,6 +22,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 namespace sv {
 namespace {
 
@@ -48,8 +50,14 @@ struct AttentionArgs {
   const uint64_t* mask;
   void* out;
   float* lse;
-  unsigned* arrivals;   // [B * groups * heads]: parts of an item that are in the workspace
-  float* parts;         // [2 * grid]: a part's sums [rows][D], maxima [rows], sums [rows]
+  struct Join* joins;   // [grid]
+  float* parts;         // [2 * grid]: a part's numbers [rows][D], references [rows], sums [rows]
+};
+
+// An item that several runs hold, written by the second of them (parts = 0 by
+// every other run): run `run` - 1 has its first part, in its second place if `side` is set.
+struct Join {
+  int b, row0, h, used, parts, side;
 };
 
 template <int DT>
@@ -409,23 +417,6 @@ struct Runs {
   }
 };
 
-// Parts of an item's result pass through the workspace past the caches that
-// work-groups on other dies do not share (cache policy sc1, as an agent-scope
-// atomic has it), 16 bytes at a time.
-constexpr int kDeviceScope = 16;
-__device__ __forceinline__ f32x4 ld_part(__amdgpu_buffer_rsrc_t rs, int byte) {
-  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, byte, 0, kDeviceScope));
-}
-__device__ __forceinline__ void st_part(__amdgpu_buffer_rsrc_t rs, int byte, f32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, byte, 0, kDeviceScope);
-}
-__device__ __forceinline__ float ld_part1(__amdgpu_buffer_rsrc_t rs, int byte) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, byte, 0, kDeviceScope));
-}
-__device__ __forceinline__ void st_part1(__amdgpu_buffer_rsrc_t rs, int byte, float v) {
-  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, byte, 0, kDeviceScope);
-}
-
 // A scalar that the loop keeps, rather than loading it from the arguments for each block.
 template <class V>
 __device__ __forceinline__ V pin(V x) {
@@ -433,16 +424,11 @@ __device__ __forceinline__ V pin(V x) {
   return x;
 }
 
-// A table entry through the scalar cache: the address is the wave's.
-__device__ __forceinline__ int scalar_at(const int32_t* p, int at) {
-  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[at];
-}
-
 // Work-groups take equal runs of units, ordered by sequence, row group,
 // key/value head and key.  An item (all keys of one group and head) that lies
 // in one run is written at once; otherwise each run's part goes to the
-// workspace, and the last to arrive joins the parts in order.  A run has at
-// most two such parts, its first and its last.
+// workspace, for join_kernel.  A run has at most two such parts, its first
+// and its last.
 template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kernel(AttentionArgs) {
   const AttentionArgs& a = kernel_arg0<AttentionArgs>();
@@ -450,7 +436,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = kQueriesShared<DT, RT> ? R * D * 2 * T : 0;
   __shared__ __align__(16) char space[kSums > kQ ? kSums : kQ];   // the queries, then the waves' results
   __shared__ float tops[kWaves][R], totals[kWaves][R];
-  __shared__ int scan[kWaves], found_start, found_entry, is_last;
+  __shared__ int scan[kWaves], found_start, found_entry;
   __shared__ Span spans[kSpans];
   float (&sums)[kWaves][16][D + 4] = *reinterpret_cast<float (*)[kWaves][16][D + 4]>(space);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -485,6 +471,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     all += scan[w];
   }
   const int U = uni(all * heads), W = min(U, (int)gridDim.x), run = blockIdx.x;
+  if (tid == 0) a.joins[run].parts = 0;
   if (run >= W) return;   // the whole work-group
   const Runs runs(U, W);
   int u = runs.start(run);
@@ -504,7 +491,6 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   __syncthreads();
   int entry = uni(found_entry), entry_start = uni(found_start);
   const Places<D> places(1 << a.c.page_log2, lane);
-  const __amdgpu_buffer_rsrc_t parts = chunk_rsrc(a.parts, (int)(2 * gridDim.x * kPart * sizeof(float)));
 
   while (u < u1) {
     const int b = entry / a.groups, rg = entry - b * a.groups;
@@ -660,7 +646,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == weight;
-    const int part = (2 * run + (u == u_begin ? 0 : 1)) * kPart;
+    float* part = a.parts + (int64_t)(2 * run + (u == u_begin ? 0 : 1)) * kPart;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt > 0) __syncthreads();   // sums is read by the tile before
@@ -694,72 +680,80 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
           if (a.lse && share == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         } else {
 #pragma unroll
-          for (int d = 0; d < S; d += 4) st_part(parts, (part + r * D + share * S + d) * 4, f32x4{v[d], v[d + 1], v[d + 2], v[d + 3]});
+          for (int d = 0; d < S; d += 4) *reinterpret_cast<f32x4*>(part + r * D + share * S + d) = f32x4{v[d], v[d + 1], v[d + 2], v[d + 3]};
           if (share == 0) {
-            st_part1(parts, (part + R * D + r) * 4, m);
-            st_part1(parts, (part + R * D + R + r) * 4, l);
+            part[R * D + r] = m;
+            part[R * D + R + r] = l;
           }
         }
       }
     }
-    if (!whole) {
+    if (tid == 0 && k0 > 0) {
       const int first = runs.of(u0), last = runs.of(u0 + weight - 1);   // the runs with a part
-      wait_mem();
-      __syncthreads();
-      if (tid == 0) {
-        unsigned* arrived = a.arrivals + (int64_t)entry * heads + h;
-        const unsigned was = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        is_last = was == (unsigned)(last - first);
-        if (is_last) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      __syncthreads();
-      if (uni(is_last)) {
-        // The first run's part is its second one unless the item starts that
-        // run.  A thread joins 4 numbers of a row; the loads of kAhead parts
-        // are in flight together.
-        constexpr int kAhead = 8, kPerRow = D / 4;
-        const int side0 = runs.start(first) < u0 ? 1 : 0;
-        for (int r = tid / kPerRow; r < used; r += kThreads / kPerRow) {
-          const int d = tid % kPerRow * 4;
-          float m = kNone, l = 0.0f;
-          f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int w = first; w <= last; w += kAhead) {
-            float pm[kAhead], pl[kAhead];
-            f32x4 pv[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-              const int x = min(w + j, last), at = (2 * x + (x == first ? side0 : 0)) * kPart;
-              pm[j] = ld_part1(parts, (at + R * D + r) * 4);
-              pl[j] = ld_part1(parts, (at + R * D + R + r) * 4);
-              pv[j] = ld_part(parts, (at + r * D + d) * 4);
-            }
-            float top = m;
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) top = fmaxf(top, pm[j]);
-            const float f0 = exp2_fast(m - top);
-            m = top;
-            l *= f0;
-            v *= f0;
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-              if (w + j <= last) {
-                const float f = exp2_fast(pm[j] - top);
-                l += pl[j] * f;
-                v += pv[j] * f;
-              }
-            }
-          }
-          const int64_t at = place_of(r);
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-          store_numbers<D, DT, 4>(a.out, at * D + d, o);
-          if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-        }
-      }
+      if (first == run - 1) a.joins[run] = {b, row0, h, used, last - first + 1, runs.start(first) < u0 ? 1 : 0};
     }
     __syncthreads();
     u = u0 + k1;
   }
+}
+
+// Joins the parts of the items that several runs hold, in order: a wave per
+// row, a lane 4 numbers of every (256 / D)-th part.
+template <int D, int DT, int RT>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
+  const AttentionArgs& a = kernel_arg0<AttentionArgs>();
+  constexpr int R = 16 * RT, kPart = R * (D + 2), kLanes = D / 4, kSplit = 64 / kLanes, kAhead = 8;
+  const Join j = a.joins[blockIdx.x];
+  const int lane = threadIdx.x & 63, r = blockIdx.y * kWaves + uni((int)(threadIdx.x >> 6));
+  if (r >= (j.parts > 0 ? j.used : 0)) return;
+  const int first = (int)blockIdx.x - 1, mine = lane / kLanes, d = lane % kLanes * 4;
+  const auto part_at = [&](int x) { return a.parts + (int64_t)(2 * (first + x) + (x == 0 ? j.side : 0)) * kPart; };
+  float m = kNone, l = 0.0f;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int x = mine; x < j.parts; x += kSplit * kAhead) {
+    float pm[kAhead], pl[kAhead];
+    f32x4 pv[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const float* p = part_at(min(x + y * kSplit, j.parts - 1));
+      pm[y] = p[R * D + r];
+      pl[y] = p[R * D + R + r];
+      pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + d);
+    }
+    float top = m;
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) top = fmaxf(top, pm[y]);
+    const float f0 = exp2_fast(m - top);
+    m = top;
+    l *= f0;
+    v *= f0;
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      if (x + y * kSplit < j.parts) {
+        const float f = exp2_fast(pm[y] - top);
+        l += pl[y] * f;
+        v += pv[y] * f;
+      }
+    }
+  }
+  const auto join2 = [&](auto swap) {   // with the lane that has the row's other parts
+    const auto max2 = [](float x, float y) { return fmaxf(x, y); };
+    const auto add2 = [](float x, float y) { return x + y; };
+    const float top = swap_combine<decltype(swap)::value>(m, max2), f = exp2_fast(m - top);
+    m = top;
+    l = swap_combine<decltype(swap)::value>(l * f, add2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = swap_combine<decltype(swap)::value>(v[e] * f, add2);
+  };
+  if constexpr (kSplit == 4) join2(std::integral_constant<int, 16>{});
+  if constexpr (kSplit >= 2) join2(std::integral_constant<int, 32>{});
+  if (mine > 0) return;
+  const int row = j.row0 + r, token = token_of(a, row);
+  const int64_t at = ((int64_t)j.b * a.c.n + token) * a.heads_q + j.h * a.group + (row - token * a.group);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+  store_numbers<D, DT, 4>(a.out, at * D + d, o);
+  if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 int check_attention(int B, int n, int heads_q, int heads, int dim) {
@@ -775,12 +769,7 @@ int check_attention(int B, int n, int heads_q, int heads, int dim) {
 
 constexpr int grid_for(int D, int dt, int rt) { return kCUs * waves_for(D, dt, rt); }
 
-// Bytes of the arrival counters: one for every item a call of these sizes can
-// have, whatever its tiles.
-size_t arrival_bytes(int B, int n, int heads_q, int heads) {
-  const int64_t groups = ((int64_t)n * (heads_q / heads) + 15) / 16;
-  return ((size_t)B * groups * heads * sizeof(unsigned) + 255) / 256 * 256;
-}
+constexpr size_t kJoinBytes = (size_t)kCUs * 4 * sizeof(Join);   // at most 4 waves per SIMD
 
 }  // namespace
 }  // namespace sv
@@ -797,7 +786,7 @@ extern "C" size_t spec_cache_attention_workspace_bytes(int B, int n, int heads_q
       parts = need > parts ? need : parts;
     }
   }
-  return arrival_bytes(B, n, heads_q, heads) + (parts + 255) / 256 * 256;
+  return (kJoinBytes + parts + 255) / 256 * 256;
 }
 
 extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int dtype, int64_t q_stride,
@@ -829,8 +818,8 @@ extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int 
   a.mask = mask;
   a.out = out;
   a.lse = lse;
-  a.arrivals = static_cast<unsigned*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + arrival_bytes(B, n, heads_q, cache->heads));
+  a.joins = static_cast<Join*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kJoinBytes);
   const int64_t rows = (int64_t)n * a.group;
   a.by_group = (unsigned)((((uint64_t)1 << 32) + a.group - 1) / a.group);
   const int dt = dtype == SPEC_BF16 ? (int)kBF16 : (int)kF32, rt = tiles_for(cache->dim, dt, rows);
@@ -840,10 +829,13 @@ extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int 
   // No more work-groups than units the call can have at most.
   const int64_t most = (int64_t)B * a.groups * cache->heads * (((int64_t)cache->table_len * cache->page + kUnitKeys - 1) / kUnitKeys + 1 + kItemUnits);
   if (most > INT_MAX) return SPEC_EINVAL;
+  const unsigned row_chunks = (unsigned)((rows < 16 * rt ? rows : 16 * rt) + kWaves - 1) / kWaves;
+  const bool split = true;
 #define SV_LAUNCH(D, DT, RT)                                                                                       \
   if (cache->dim == D && dt == (int)DT && rt == RT) {                                                              \
     const int grid = (int)(most < grid_for(D, DT, RT) ? most : grid_for(D, DT, RT));                               \
     hipLaunchKernelGGL((attention_kernel<D, DT, RT>), dim3(grid), dim3(kThreads), 0, st, a);                       \
+    if (split) hipLaunchKernelGGL((join_kernel<D, DT, RT>), dim3(grid, row_chunks), dim3(kThreads), 0, st, a);     \
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;                                               \
   }
   SV_LAUNCH(64, kBF16, 1) SV_LAUNCH(64, kBF16, 2) SV_LAUNCH(64, kBF16, 3) SV_LAUNCH(64, kBF16, 4)

@@ -25,50 +25,91 @@ __device__ void report(const CacheView& c, int b, int32_t* status) {
   if (threadIdx.x == 0) status[b] = s.count < 0 ? 1 : bad ? 2 : 0;
 }
 
-struct AppendArgs {
+// A wave takes a tile of 16 positions of one sequence and head, its keys and
+// its values, as the attention's waves read them: lane (g, i) holds 4 tokens,
+// 4 g to 4 g + 3, of D / 16 numbers from i * D / 16 on.  The values' codes of
+// a lane then lie side by side in the record, every access of a row is
+// contiguous over 16 lanes, and what depends on the sequence is scalar.
+struct TileArgs {
   CacheView c;
   const void* k;
   const void* v;
   int64_t k_stride, v_stride;
+  void* out_k;
+  void* out_v;
   int32_t* status;
-  int blocks;   // work-groups per half (keys, values); those behind write the status
+  int tiles;    // that n tokens of a sequence can touch
+  int blocks;   // work-groups; those behind write the status
 };
 
-// One thread per 8 numbers; the 4 threads of a block of 32 are neighbours in
-// a wave and share its largest magnitude through two quad permutes.  Bound by
-// memory: 8 numbers in, 4 bytes and a quarter of a scale out.
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
-  using F = Format<D>;
-  const CacheView& c = a.c;
-  if ((int)blockIdx.x >= 2 * a.blocks) return report(c, (int)blockIdx.x - 2 * a.blocks, a.status);
-  const bool values = (int)blockIdx.x >= a.blocks;
-  const unsigned per_token = (unsigned)c.heads * (D / 8);
-  const unsigned unit = ((unsigned)blockIdx.x - (values ? a.blocks : 0)) * kThreads + threadIdx.x;
-  const unsigned token = unit / per_token, in_token = unit - token * per_token;
-  // per_token is a multiple of 8, so the four threads of a block leave together.
-  if (token >= (unsigned)c.B * (unsigned)c.n) return;
-  const int b = token / (unsigned)c.n, i = token - b * c.n;
-  const Span s = span_of(c, b);
-  if (i >= s.count) return;
-  const int t = s.pos + i;
-  const int page = page_of(c, b, t);
-  if (page < 0) return;
-  const int h = in_token / (D / 8), d0 = (in_token % (D / 8)) * 8;
+struct Tile {
+  int b, h, token0, r0, page;   // token0: the call's token at the tile's first position (may be negative)
+  int count;                    // tokens of the sequence, -1 after a range error
+};
 
-  float x[8];
-  load_row8<DT>(values ? a.v : a.k, (int64_t)token * (values ? a.v_stride : a.k_stride) + h * D + d0, x);
+// The wave's tile; false if it has none.
+__device__ __forceinline__ bool tile_of(const TileArgs& a, Tile& t) {
+  const CacheView& c = a.c;
+  const unsigned wave = blockIdx.x * kWaves + (unsigned)uni((int)(threadIdx.x >> 6));
+  const unsigned row = wave / (unsigned)c.heads, seq = row / (unsigned)a.tiles;
+  if (seq >= (unsigned)c.B) return false;
+  t.b = (int)seq;
+  t.h = (int)(wave - row * (unsigned)c.heads);
+  const int tile = (int)(row - seq * (unsigned)a.tiles);
+  const int64_t pos = (int64_t)(c.len ? scalar_at(c.len, t.b) : 0) - c.lag;
+  const Span s = span_from(c, pos, c.count ? scalar_at(c.count, t.b) : c.n);
+  t.count = s.count;
+  const int start = (s.pos & ~15) + 16 * tile;
+  t.token0 = start - s.pos;
+  if (t.token0 >= (s.count < 0 ? c.n : s.count)) return false;
+  t.r0 = start & ((1 << c.page_log2) - 1);
+  t.page = -1;
+  if (s.count >= 0) {
+    const int page = scalar_at(c.table + (int64_t)t.b * c.table_len, start >> c.page_log2);
+    if (page >= 0 && page < c.pages) t.page = page;
+  }
+  return true;
+}
+
+// op over the lanes that hold a block of 32 numbers.
+template <int D, class V, class Op>
+__device__ __forceinline__ V over_block(V x, Op op) {
+  x = op(x, dpp<kDppQuad1032>(x, x));
+  if constexpr (D <= 128) x = op(x, dpp<kDppQuad2301>(x, x));
+  if constexpr (D == 64) x = op(x, dpp<kDppRowHalfMirror>(x, x));
+  return x;
+}
+
+// D / 16 numbers of a row whose first lies anywhere its type's alignment allows.
+template <int N>
+struct __attribute__((packed, aligned(2))) Bf16xN { uint16_t w[N]; };
+template <int N>
+struct __attribute__((packed, aligned(4))) F32xN { float v[N]; };
+template <int DT, int N>
+__device__ __forceinline__ void load_row(const void* row, int64_t j, float (&x)[N]) {
+  if constexpr (DT == kBF16) {
+    const Bf16xN<N> t = *reinterpret_cast<const Bf16xN<N>*>(static_cast<const uint16_t*>(row) + j);
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = __uint_as_float((uint32_t)t.w[e] << 16);
+  } else {
+    const F32xN<N> t = *reinterpret_cast<const F32xN<N>*>(static_cast<const float*>(row) + j);
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = t.v[e];
+  }
+}
+
+// The codes of a lane's N numbers of one token, and the scale byte of their block.
+template <int D, int N>
+__device__ __forceinline__ unsigned quantise(const float (&x)[N], uint32_t (&w)[(N + 7) / 8]) {
   float m = 0.0f;
   int odd = 0;   // a NaN or an infinity
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < N; ++e) {
     m = fmaxf(m, fabsf(x[e]));
     odd |= !(fabsf(x[e]) <= FLT_MAX);
   }
-  m = fmaxf(m, dpp<kDppQuad1032>(m, m));
-  m = fmaxf(m, dpp<kDppQuad2301>(m, m));
-  odd |= dpp<kDppQuad1032>(odd, odd);
-  odd |= dpp<kDppQuad2301>(odd, odd);
+  m = over_block<D>(m, [](float u, float v) { return fmaxf(u, v); });
+  odd = over_block<D>(odd, [](int u, int v) { return u | v; });
   // a = f 2^(E - 127), 1 <= f < 2: the smallest power of two s with a <= 7 s
   // is 2^(E - 129) up to f = 1.75 and 2^(E - 128) above.  Below the normal
   // range E = 0 and the clamp decides.
@@ -76,104 +117,214 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   int e = (int)(bits >> 23) - 2 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   e = e < 3 ? 3 : e > 252 ? 252 : e;
   const float scale = scale_of((unsigned)e);
-  uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
-  if (odd) w = 0;
-
-  const int P = 1 << c.page_log2, r = t & (P - 1);
-  uint8_t* rec = c.data + ((int64_t)page * c.heads + h) * F::record(P);
-  if (!values) {
-    *reinterpret_cast<uint32_t*>(rec + F::keys(r) + d0 / 2) = w;
-    if ((d0 & 31) == 0) rec[F::key_scales(P, r) + d0 / 32] = (uint8_t)(odd ? kNaNScale : e);
-  } else {
-    const int share = d0 / (D / 16);
-    uint8_t* at = rec + F::values(P, r, share);
-    if constexpr (D == 64) {   // two shares of 4 numbers
-      *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
-      *reinterpret_cast<uint16_t*>(at + 4 * F::kPiece) = (uint16_t)(w >> 16);
-    } else {
-      *reinterpret_cast<uint32_t*>(at + (d0 % (D / 16)) / 2) = w;
+#pragma unroll
+  for (int q = 0; q < (N + 7) / 8; ++q) {
+    uint32_t y = 0;
+    y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x[8 * q], x[8 * q + 1], scale, 0);
+    y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x[8 * q + 2], x[8 * q + 3], scale, 1);
+    if constexpr (N > 4) {
+      y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x[8 * q + 4], x[8 * q + 5], scale, 2);
+      y = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(y, x[8 * q + 6], x[8 * q + 7], scale, 3);
     }
-    if ((d0 & 31) == 0) rec[F::value_scale(P, r, d0 / 32)] = (uint8_t)(odd ? kNaNScale : e);
+    w[q] = odd ? 0 : y;
+  }
+  return odd ? (unsigned)kNaNScale : (unsigned)e;
+}
+
+// Codes of N numbers at p: N / 2 bytes.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[(N + 7) / 8]) {
+  if constexpr (N == 4) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+  } else if constexpr (N == 8) {
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+  } else {
+    *reinterpret_cast<uint64_t*>(p) = (uint64_t)w[1] << 32 | w[0];
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[(N + 7) / 8]) {
+  if constexpr (N == 4) {
+    w[0] = *reinterpret_cast<const uint16_t*>(p);
+  } else if constexpr (N == 8) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    const uint64_t t = *reinterpret_cast<const uint64_t*>(p);
+    w[0] = (uint32_t)t;
+    w[1] = (uint32_t)(t >> 32);
   }
 }
 
-struct ReadArgs {
-  CacheView c;
-  void* out_k;
-  void* out_v;
-  int32_t* status;
-  int blocks;
-};
+// Bound by memory: a number in, 4 bits and a 32nd of a byte out.
+template <int D, int DT>
+__global__ __launch_bounds__(kThreads) void append_kernel(TileArgs a) {
+  using F = Format<D>;
+  constexpr int N = D / 16;
+  const CacheView& c = a.c;
+  if ((int)blockIdx.x >= a.blocks) return report(c, (int)blockIdx.x - a.blocks, a.status);
+  Tile t;
+  if (!tile_of(a, t) || t.page < 0) return;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, P = 1 << c.page_log2;
+  uint8_t* rec = c.data + ((int64_t)t.page * c.heads + t.h) * F::record(P);
+  const int64_t first = (int64_t)t.b * c.n + t.token0 + 4 * g, in = (int64_t)t.h * D + i * N;
+  const bool scales = i % (32 / N) == 0;   // the block's first lane writes its scale
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const void* src = half ? a.v : a.k;
+    const int64_t stride = half ? a.v_stride : a.k_stride;
+    float x[4][N];
+    bool live[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // lanes of one token leave or stay together
+      const int token = t.token0 + 4 * g + j;
+      live[j] = token >= 0 && token < t.count;
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[j][e] = 0.0f;
+      if (live[j]) load_row<DT, N>(src, (first + j) * stride + in, x[j]);
+    }
+    uint32_t w[4][(N + 7) / 8];
+    unsigned sc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sc[j] = quantise<D, N>(x[j], w[j]);
+    const int r = t.r0 + 4 * g;
+    if (half == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!live[j]) continue;
+        store_codes<N>(rec + F::keys(r + j) + i * (N / 2), w[j]);
+        if (scales) rec[F::key_scales(P, r + j) + i / (32 / N)] = (uint8_t)sc[j];
+      }
+    } else if (live[0] && live[1] && live[2] && live[3]) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(rec + F::values(P, r, i));
+      if constexpr (N == 4) {
+        at[0] = w[0][0] | w[1][0] << 16;
+        at[1] = w[2][0] | w[3][0] << 16;
+      } else {
+#pragma unroll
+        for (int q = 0; q < N / 8; ++q)
+          reinterpret_cast<u32x4*>(at)[q] = N == 8 ? u32x4{w[0][0], w[1][0], w[2][0], w[3][0]}
+                                                   : u32x4{w[2 * q][0], w[2 * q][N / 8 - 1], w[2 * q + 1][0], w[2 * q + 1][N / 8 - 1]};
+      }
+      if (scales)
+        *reinterpret_cast<uint32_t*>(rec + F::value_scale(P, r, i / (32 / N))) = sc[0] | sc[1] << 8 | sc[2] << 16 | sc[3] << 24;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!live[j]) continue;
+        store_codes<N>(rec + F::values(P, r + j, i), w[j]);
+        if (scales) rec[F::value_scale(P, r + j, i / (32 / N))] = (uint8_t)sc[j];
+      }
+    }
+  }
+}
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// One thread per 8 numbers, as append.
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
-  using F = Format<D>;
-  const CacheView& c = a.c;
-  if ((int)blockIdx.x >= 2 * a.blocks) return report(c, (int)blockIdx.x - 2 * a.blocks, a.status);
-  const bool values = (int)blockIdx.x >= a.blocks;
-  const unsigned per_token = (unsigned)c.heads * (D / 8);
-  const unsigned unit = ((unsigned)blockIdx.x - (values ? a.blocks : 0)) * kThreads + threadIdx.x;
-  const unsigned token = unit / per_token, in_token = unit - token * per_token;
-  if (token >= (unsigned)c.B * (unsigned)c.n) return;
-  const int b = token / (unsigned)c.n, i = token - b * c.n;
-  const Span s = span_of(c, b);
-  if (s.count >= 0 && i >= s.count) return;
-  const int h = in_token / (D / 8), d0 = (in_token % (D / 8)) * 8;
-  const int t = s.pos + i;
-  const int page = s.count < 0 ? -1 : page_of(c, b, t);
-  float x[8];
-  unsigned e = kNaNScale;
-  uint32_t w = 0;
-  if (page >= 0) {
-    const int P = 1 << c.page_log2, r = t & (P - 1);
-    const uint8_t* rec = c.data + ((int64_t)page * c.heads + h) * F::record(P);
-    if (!values) {
-      w = *reinterpret_cast<const uint32_t*>(rec + F::keys(r) + d0 / 2);
-      e = rec[F::key_scales(P, r) + d0 / 32];
-    } else {
-      const uint8_t* at = rec + F::values(P, r, d0 / (D / 16));
-      if constexpr (D == 64) {
-        w = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + 4 * F::kPiece) << 16;
-      } else {
-        w = *reinterpret_cast<const uint32_t*>(at + (d0 % (D / 16)) / 2);
-      }
-      e = rec[F::value_scale(P, r, d0 / 32)];
-    }
-  }
+// A token's N numbers to its row.  In bfloat16 they are exact: 2 significant
+// bits, and the scale keeps them in the normal range.
+template <int DT, int N>
+__device__ __forceinline__ void store_row(void* out, int64_t at, const uint32_t (&w)[(N + 7) / 8], unsigned e) {
   const float scale = scale_of(e);
-  const f32x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0);
-  const f32x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
-  const f32x2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2);
-  const f32x2 y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
-  x[0] = y0.x; x[1] = y0.y; x[2] = y1.x; x[3] = y1.y;
-  x[4] = y2.x; x[5] = y2.y; x[6] = y3.x; x[7] = y3.y;
-  if (e == kNaNScale) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(0x7FC00000u);
-  }
-  void* out = values ? a.out_v : a.out_k;
-  const int64_t at = (int64_t)unit * 8;
   if constexpr (DT == kBF16) {
-    // Exact: 2 significant bits, and the scale keeps it in the normal range.
-    u32x4 o;
+    uint32_t y[N / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = (__float_as_uint(x[2 * j]) >> 16) | (__float_as_uint(x[2 * j + 1]) & 0xFFFF0000u);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) = o;
+    for (int q = 0; q < (N + 7) / 8; ++q) {
+      y[4 * q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], scale, 0));
+      y[4 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], scale, 1));
+      if constexpr (N > 4) {
+        y[4 * q + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], scale, 2));
+        y[4 * q + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[q], scale, 3));
+      }
+    }
+    if (e == kNaNScale) {
+#pragma unroll
+      for (int q = 0; q < N / 2; ++q) y[q] = 0x7FC07FC0u;
+    }
+    uint16_t* p = static_cast<uint16_t*>(out) + at;
+    if constexpr (N == 4) {
+      *reinterpret_cast<uint64_t*>(p) = (uint64_t)y[1] << 32 | y[0];
+    } else {
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q)
+        __builtin_nontemporal_store(u32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]}, reinterpret_cast<u32x4*>(p) + q);
+    }
   } else {
-    f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at);
-    p[0] = f32x4{x[0], x[1], x[2], x[3]};
-    p[1] = f32x4{x[4], x[5], x[6], x[7]};
+    float y[N];
+#pragma unroll
+    for (int q = 0; q < (N + 7) / 8; ++q) {
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], scale, 1);
+      y[8 * q] = a.x; y[8 * q + 1] = a.y; y[8 * q + 2] = b.x; y[8 * q + 3] = b.y;
+      if constexpr (N > 4) {
+        const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[q], scale, 3);
+        y[8 * q + 4] = c.x; y[8 * q + 5] = c.y; y[8 * q + 6] = d.x; y[8 * q + 7] = d.y;
+      }
+    }
+    if (e == kNaNScale) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) y[q] = __uint_as_float(0x7FC00000u);
+    }
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q)
+      __builtin_nontemporal_store(f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]}, reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) + q);
   }
 }
 
-template <class Args, class Launch>
+// Bound by memory: the rows that it writes.
+template <int D, int DT>
+__global__ __launch_bounds__(kThreads) void read_kernel(TileArgs a) {
+  using F = Format<D>;
+  constexpr int N = D / 16, W = (N + 7) / 8;
+  const CacheView& c = a.c;
+  if ((int)blockIdx.x >= a.blocks) return report(c, (int)blockIdx.x - a.blocks, a.status);
+  Tile t;
+  if (!tile_of(a, t)) return;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, P = 1 << c.page_log2;
+  const uint8_t* rec = c.data + ((int64_t)max(t.page, 0) * c.heads + t.h) * F::record(P);
+  const int live = t.count < 0 ? c.n : t.count, r = t.r0 + 4 * g, blk = i / (32 / N);
+  const int64_t row0 = ((int64_t)t.b * c.n + t.token0 + 4 * g) * c.heads + t.h;
+  uint32_t k[4][W], v[4][W];
+  unsigned ks[4], vs[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int q = 0; q < W; ++q) k[j][q] = v[j][q] = 0;
+    ks[j] = vs[j] = kNaNScale;
+  }
+  if (t.page >= 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      load_codes<N>(rec + F::keys(r + j) + i * (N / 2), k[j]);
+      ks[j] = rec[F::key_scales(P, r + j) + blk];
+    }
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(rec + F::values(P, r, i));
+    if constexpr (N == 4) {
+      const uint64_t x = *reinterpret_cast<const uint64_t*>(at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j][0] = (uint32_t)(x >> (16 * j)) & 0xFFFFu;
+    } else {
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q) {
+        const u32x4 x = reinterpret_cast<const u32x4*>(at)[q];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[(4 * q + y) / W][(4 * q + y) % W] = x[y];
+      }
+    }
+    const uint32_t s4 = *reinterpret_cast<const uint32_t*>(rec + F::value_scale(P, r, blk));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vs[j] = s4 >> (8 * j) & 255;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int token = t.token0 + 4 * g + j;
+    if (token < 0 || token >= live) continue;
+    const int64_t to = (row0 + (int64_t)j * c.heads) * D + i * N;
+    store_row<DT, N>(a.out_k, to, k[j], ks[j]);
+    store_row<DT, N>(a.out_v, to, v[j], vs[j]);
+  }
+}
+
+template <class Launch>
 int by_dim_and_type(int dim, int dtype, Launch launch) {
   (void)hipGetLastError();
   const bool bf = dtype == SPEC_BF16;
@@ -185,10 +336,11 @@ int by_dim_and_type(int dim, int dtype, Launch launch) {
   return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;
 }
 
-// Work-groups for B * n tokens' keys (or values).  check_cache keeps the units within 31 bits.
+// Tiles of 16 positions that n tokens can touch, and work-groups for B
+// sequences' tiles: at most B * n * heads waves, which check_cache keeps within 28 bits.
+int tiles_of(int n) { return (n + 14) / 16 + 1; }
 int blocks_for(const spec_cache* c, int B, int n) {
-  const int64_t units = (int64_t)B * n * c->heads * (c->dim / 8);
-  return (int)((units + kThreads - 1) / kThreads);
+  return (int)(((int64_t)B * tiles_of(n) * c->heads + kWaves - 1) / kWaves);
 }
 
 }  // namespace
@@ -209,9 +361,9 @@ extern "C" int spec_cache_append(const spec_cache* cache, const void* k, const v
   const uintptr_t es = dtype == SPEC_BF16 ? 2 : 4;
   if (!k || !v || ((uintptr_t)k % es) || ((uintptr_t)v % es)) return SPEC_EINVAL;
   const int blocks = blocks_for(cache, B, n);
-  const AppendArgs a{view_of(cache, len, lag, count, B, n), k, v, k_stride, v_stride, status, blocks};
-  const dim3 grid(2 * blocks + (status ? B : 0));
-  return by_dim_and_type<AppendArgs>(cache->dim, dtype, [&](auto d, auto t) {
+  const TileArgs a{view_of(cache, len, lag, count, B, n), k, v, k_stride, v_stride, nullptr, nullptr, status, tiles_of(n), blocks};
+  const dim3 grid(blocks + (status ? B : 0));
+  return by_dim_and_type(cache->dim, dtype, [&](auto d, auto t) {
     hipLaunchKernelGGL((append_kernel<decltype(d)::value, decltype(t)::value>), grid, dim3(kThreads), 0,
                        static_cast<hipStream_t>(stream), a);
   });
@@ -226,9 +378,9 @@ extern "C" int spec_cache_read(const spec_cache* cache, const int32_t* len, int 
   if (const int st = check_buffers(cache)) return st;
   if (!out_k || !out_v || off16(out_k) || off16(out_v)) return SPEC_EINVAL;
   const int blocks = blocks_for(cache, B, n);
-  const ReadArgs a{view_of(cache, len, lag, count, B, n), out_k, out_v, status, blocks};
-  const dim3 grid(2 * blocks + (status ? B : 0));
-  return by_dim_and_type<ReadArgs>(cache->dim, dtype, [&](auto d, auto t) {
+  const TileArgs a{view_of(cache, len, lag, count, B, n), nullptr, nullptr, 0, 0, out_k, out_v, status, tiles_of(n), blocks};
+  const dim3 grid(blocks + (status ? B : 0));
+  return by_dim_and_type(cache->dim, dtype, [&](auto d, auto t) {
     hipLaunchKernelGGL((read_kernel<decltype(d)::value, decltype(t)::value>), grid, dim3(kThreads), 0,
                        static_cast<hipStream_t>(stream), a);
   });

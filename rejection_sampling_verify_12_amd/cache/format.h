@@ -48,12 +48,18 @@ struct Span {   // one sequence's tokens in a call
   int count;    // tokens, or -1 after a range error
 };
 
-__device__ __forceinline__ Span span_of(const CacheView& c, int b) {
-  const int64_t pos = (int64_t)(c.len ? c.len[b] : 0) - c.lag;
-  const int count = c.count ? c.count[b] : c.n;
+__device__ __forceinline__ Span span_from(const CacheView& c, int64_t pos, int count) {
   const int64_t room = (int64_t)c.table_len << c.page_log2;
   if (count < 0 || count > c.n || (count > 0 && (pos < 0 || pos + count > room))) return {0, -1};
   return {count > 0 ? (int)pos : 0, count};
+}
+__device__ __forceinline__ Span span_of(const CacheView& c, int b) {
+  return span_from(c, (int64_t)(c.len ? c.len[b] : 0) - c.lag, c.count ? c.count[b] : c.n);
+}
+
+// An entry of an array that the kernel does not write, through the scalar cache: the address is the wave's.
+__device__ __forceinline__ int scalar_at(const int32_t* p, int at) {
+  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[at];
 }
 
 // Eight numbers of a row whose first lies anywhere its type's alignment allows.
