@@ -33,7 +33,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 32;               // keys per wave and step
 constexpr int kUnitKeys = kWaves * kBlock;   // keys per work-group and step
-constexpr int kItemUnits = 4;
+constexpr int kItemUnits = 6;
 constexpr int kCUs = 256;                // MI355X
 constexpr int kSpans = 512;              // sequences whose positions a work-group keeps in shared memory
 
@@ -301,6 +301,21 @@ __device__ __forceinline__ uint32_t find_nan_keys(uint32_t k0, uint32_t k1, uint
   return found;
 }
 
+// Bit k: the row whose token is at position `at` sees key p + k.
+__device__ __forceinline__ uint32_t seen_keys(const AttentionArgs& a, const Item& it, int b, int at, int p) {
+  const auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };   // bits 0 .. n - 1
+  const int token = at - it.s.pos;
+  if (token >= it.s.count) return 0;
+  uint32_t sees = below(at + 1 - p);
+  if (a.mask) {
+    const int first = it.s.pos - p;   // of the new tokens, in the block
+    uint64_t bits = a.mask[(int64_t)b * a.c.n + token];
+    bits &= it.s.count >= 64 ? ~0ull : (1ull << it.s.count) - 1;
+    sees = below(first) | (uint32_t)(first >= 32 || first <= -64 ? 0 : first >= 0 ? bits << first : bits >> -first);
+  }
+  return a.window > 0 ? sees & ~below(at - a.window + 1 - p) : sees;
+}
+
 // Weights of a block and the running maximum and sum.  `masked`: some row does not see some key.
 template <int D, int DT, int RT>
 __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& it, int b, int p, int lane, bool masked,
@@ -315,17 +330,12 @@ __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& 
     if (masked || nan_keys) {
       int at = it.s.pos + rows.token[rt], g4 = 4 * g;
       asm volatile("" : "+v"(at), "+v"(g4));   // computed here, not kept over the loop
-      const int token = at - it.s.pos;
-      const bool used = token < it.s.count;
-      const int last = !used ? -1 : a.mask ? it.s.pos - 1 : at;
-      const uint64_t bits = (a.mask && used) ? a.mask[(int64_t)b * a.c.n + token] : 0;
-      const int first = a.window > 0 ? at - a.window + 1 : 0;
+      const uint32_t sees = seen_keys(a, it, b, at, p);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int in = 16 * (e >> 2) + g4 + (e & 3), key = p + in, j = key - it.s.pos;
-        const bool sees = key >= first && (key <= last || (j >= 0 && j < it.s.count && (bits >> j & 1)));
-        if (nan_keys >> in & 1) x[e] = __uint_as_float(0x7FC00000u);
-        x[e] = sees ? x[e] : -INFINITY;
+        const int in = 16 * (e >> 2) + (e & 3);
+        if (nan_keys) x[e] = nan_keys >> (in + g4) & 1 ? __uint_as_float(0x7FC00000u) : x[e];
+        x[e] = sees >> (in + g4) & 1 ? x[e] : -INFINITY;
       }
     }
     // The reference m only has to keep 2^(x - m) in range, so it moves when a
