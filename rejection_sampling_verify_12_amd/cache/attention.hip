@@ -427,6 +427,18 @@ struct Runs {
   }
 };
 
+// Inclusive prefix sum over the wave (every lane active).
+__device__ __forceinline__ int inclusive_scan(int v) {
+  int s = v + dpp<kDppRowShr + 1, 0xF, 0xF, true>(v, 0);
+  s += dpp<kDppRowShr + 2, 0xF, 0xF, true>(v, 0);
+  s += dpp<kDppRowShr + 3, 0xF, 0xF, true>(v, 0);   // rows: sums of 4
+  s += dpp<kDppRowShr + 4, 0xF, 0xE>(s, 0);         // lanes 4..15 of a row
+  s += dpp<kDppRowShr + 8, 0xF, 0xC>(s, 0);         // lanes 8..15
+  s += dpp<kDppRowBcast15, 0xA>(s, 0);              // rows 1, 3
+  s += dpp<kDppRowBcast31, 0xC>(s, 0);              // rows 2, 3
+  return s;
+}
+
 // A scalar that the loop keeps, rather than loading it from the arguments for each block.
 template <class V>
 __device__ __forceinline__ V pin(V x) {
@@ -446,60 +458,58 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = kQueriesShared<DT, RT> ? R * D * 2 * T : 0;
   __shared__ __align__(16) char space[kSums > kQ ? kSums : kQ];   // the queries, then the waves' results
   __shared__ float tops[kWaves][R], totals[kWaves][R];
-  __shared__ int scan[kWaves], found_start, found_entry;
   __shared__ Span spans[kSpans];
   float (&sums)[kWaves][16][D + 4] = *reinterpret_cast<float (*)[kWaves][16][D + 4]>(space);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int heads = a.c.heads, entries = a.c.B * a.groups;
 
-  for (int b = tid; b < min(a.c.B, kSpans); b += kThreads) spans[b] = span_of(a.c, b);
-  __syncthreads();
+  // Every wave finds its run by itself (each writes the same positions and
+  // reads its own), so the work-group starts without a barrier.
+  {
+    int len[kSpans / 64], count[kSpans / 64];   // all loads before the first use
+#pragma unroll
+    for (int q = 0; q < kSpans / 64; ++q) {
+      const int b = min(lane + 64 * q, a.c.B - 1);
+      if (64 * q >= a.c.B) break;
+      len[q] = a.c.len ? a.c.len[b] : 0;
+      count[q] = a.c.count ? a.c.count[b] : a.c.n;
+    }
+#pragma unroll
+    for (int q = 0; q < kSpans / 64; ++q) {
+      if (64 * q >= a.c.B) break;
+      if (lane + 64 * q < a.c.B) spans[lane + 64 * q] = span_from(a.c, (int64_t)len[q] - a.c.lag, count[q]);
+    }
+  }
   const auto span_at = [&](int b) { return b < kSpans ? spans[b] : span_of(a.c, b); };
   const auto weight_at = [&](int entry) {
     const int b = entry / a.groups;
     return item_of(a, span_at(b), entry - b * a.groups, R).weight();
   };
-  // Weight of one head before this thread's entries, and in all (the host keeps them within 31 bits).
-  const int per = (entries + kThreads - 1) / kThreads;
-  const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+  // Weight of one head before this lane's entries, and in all (the host keeps them within 31 bits).
+  const int per = (entries + 63) / 64;
+  const int e0 = min(lane * per, entries), e1 = min(e0 + per, entries);
   int mine = 0;
   for (int e = e0; e < e1; ++e) mine += weight_at(e);
-  int before = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(before, off);
-    if (lane >= off) before += o;
-  }
-  if (lane == 63) scan[wave] = before;
-  __syncthreads();
-  before -= mine;
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += scan[w];
-    all += scan[w];
-  }
-  const int U = uni(all * heads), W = min(U, (int)gridDim.x), run = blockIdx.x;
+  const int through = inclusive_scan(mine), before = through - mine;
+  const int U = __builtin_amdgcn_readlane(through, 63) * heads, W = min(U, (int)gridDim.x), run = blockIdx.x;
   if (tid == 0) a.joins[run].parts = 0;
   if (run >= W) return;   // the whole work-group
   const Runs runs(U, W);
   int u = runs.start(run);
   const int u1 = runs.start(run + 1), u_begin = u;
-  if (before * heads <= u && u < (before + mine) * heads) {
-    int start = before * heads;
+  int found = 0, start = before * heads;
+  const bool here = start <= u && u < through * heads;
+  if (here) {
     for (int e = e0; e < e1; ++e) {
-      const int units = weight_at(e) * heads;
-      if (u < start + units) {
-        found_entry = e;
-        found_start = start;
-        break;
-      }
-      start += units;
+      const int weight = weight_at(e) * heads;
+      found = e;
+      if (u < start + weight) break;
+      start += weight;
     }
   }
-  __syncthreads();
-  int entry = uni(found_entry), entry_start = uni(found_start);
+  const int at = __ffsll((unsigned long long)__ballot(here)) - 1;   // one lane's entries hold the run's start
+  int entry = __builtin_amdgcn_readlane(found, at), entry_start = __builtin_amdgcn_readlane(start, at);
   const Places<D> places(1 << a.c.page_log2, lane);
 
   while (u < u1) {
