@@ -68,11 +68,13 @@ class RefRound:
 
 def sd_rounds(draft64: np.ndarray, target64: np.ndarray, noise: np.ndarray, last0, len0,
               u_accept: np.ndarray, u_sample: np.ndarray, T: float, rounds: int,
-              seqs=None) -> list[RefRound]:
+              seqs=None, layer=None) -> list[RefRound]:
     """``rounds`` rounds from the start state (last0, len0) for the sequences
     ``seqs`` (default: all).  draft64, target64: [H, V] float64 tables (exact
     values of the stored logits); u_accept [R, B, gamma], u_sample
-    [R, B, gamma+1]."""
+    [R, B, gamma+1].  layer(b, length, tokens): the target's further logits
+    [gamma+1, V] for the tokens last, x_0 .. x_{gamma-1} of sequence b, the
+    first of them at position length - 1."""
     B = len(last0)
     seqs = list(range(B)) if seqs is None else list(seqs)
     gamma = u_accept.shape[2]
@@ -89,6 +91,8 @@ def sd_rounds(draft64: np.ndarray, target64: np.ndarray, noise: np.ndarray, last
         for b in seqs:
             p = bigram_rows(draft64, last[b], x[b])
             q = bigram_rows(target64, last[b], x[b])
+            if layer is not None:
+                q = q + layer(b, int(length[b]), [int(last[b])] + [int(v) for v in x[b]])
             res: SeqResult = verify_one(p, q, x[b], u_accept[r, b], u_sample[r, b], T,
                                         in_len=int(length[b]))
             rec.x[b] = x[b]

@@ -34,16 +34,86 @@ drafts; nothing goes through the host between rounds.
   afresh on a miss).
 
 Both schedules emit the same tokens, round for round.
+
+With a ``TargetAttention`` the target is a bigram table plus one attention
+layer over a key/value cache in 4 bits: a round's gamma + 1 tokens are
+quantised into the cache, their queries attend over everything the sequence
+holds, and the projected result is added to the table's logits.  A rejection
+moves only the length (the summary's AMD MI300X part: rollback of the KV
+cache): the next round's tokens overwrite the rejected ones' places.
 """
 from __future__ import annotations
 
 import dataclasses
 import time
 
-from . import (PredictOut, VerifyOut, alloc_outputs, alloc_predict_outputs, new_workspace,
+from . import (AttentionOut, PredictOut, QuantCache, VerifyOut, alloc_outputs, alloc_predict_outputs, new_cache,
+               new_workspace, spec_cache_append, spec_cache_attention, spec_cache_attention_workspace_bytes,
                spec_predict_outcomes, spec_predict_workspace_bytes, spec_ssd_advance,
                spec_ssd_prespeculate, spec_synth_draft, spec_synth_rows, spec_synthetic_busy,
                spec_verify, spec_verify_predict, spec_workspace_bytes, _dtype_code)
+
+
+@dataclasses.dataclass
+class TargetAttention:
+    """One attention layer of the target over a 4-bit key/value cache.
+
+    q_table [H, heads_q * dim], k_table and v_table [H, heads * dim]: a token's
+    query, keys and values are row t mod H; proj [heads_q * dim, V]: its result's
+    share of the logits; all of the target table's dtype, the first three with one H.  history [B, n] int32:
+    the tokens at positions 0 .. len0 - 2 (the one at len0 - 1 is last0).
+    scale: of the scores, 1/sqrt(dim) by default.  page: tokens per cache page.
+    """
+    q_table: object
+    k_table: object
+    v_table: object
+    proj: object
+    heads: int
+    dim: int
+    history: object
+    scale: float | None = None
+    page: int = 64
+
+
+class _Attention:
+    """A run's cache and buffers of a TargetAttention, and its pass per round."""
+
+    def __init__(self, t: TargetAttention, m: "Models", rounds: int):
+        import torch
+        self.t, B, n = t, m.B, m.gamma + 1
+        dev, dt = t.q_table.device, t.q_table.dtype
+        self.heads_q = t.q_table.shape[1] // t.dim
+        # Room for every token a run can commit and the last round's drafts.
+        most = int(m.len0.max()) + (rounds + 1) * n
+        pages = -(-most // t.page)
+        table = torch.arange(B * pages, dtype=torch.int32, device=dev).view(B, pages)
+        self.cache: QuantCache = new_cache(B * pages, t.heads, t.dim, table, t.page)
+        rows = lambda heads: torch.empty((B, n, heads, t.dim), dtype=dt, device=dev)
+        self.q, self.k, self.v = rows(self.heads_q), rows(t.heads), rows(t.heads)
+        self.out = AttentionOut(rows(self.heads_q), None)
+        self.token, self.row = (torch.empty((B, n), dtype=torch.int32, device=dev) for _ in range(2))
+        self.ws = new_workspace(spec_cache_attention_workspace_bytes(B, n, self.heads_q, t.heads, t.dim), dev)
+        h = t.history.shape[1]
+        if h:
+            at = t.history.long() % t.k_table.shape[0]
+            kv = [x[at].view(B, h, t.heads, t.dim) for x in (t.k_table, t.v_table)]
+            spec_cache_append(self.cache, *kv, count=(m.len0 - 1).to(torch.int32))
+
+    def add_to(self, logits, last, length, x, stream):
+        """The layer over the round's tokens (last, x_0 .. x_{gamma-1}, from position length - 1 on), added to its
+        logits [B, gamma+1, V], on ``stream``, the current one.  (A token of -1 takes the last row: the table's
+        logits after it are NaN already.)"""
+        import torch
+        t, B, n = self.t, x.shape[0], x.shape[1] + 1
+        self.token[:, 0].copy_(last)
+        self.token[:, 1:].copy_(x)
+        torch.remainder(self.token, t.q_table.shape[0], out=self.row)
+        for table, to in ((t.q_table, self.q), (t.k_table, self.k), (t.v_table, self.v)):
+            torch.index_select(table, 0, self.row.view(-1), out=to.view(B * n, -1))
+        spec_cache_append(self.cache, self.k, self.v, length, lag=1, stream=stream)
+        spec_cache_attention(self.cache, self.q, length, lag=1, scale=t.scale, out=self.out, workspace=self.ws,
+                             stream=stream)
+        logits.view(B * n, -1).addmm_(self.out.out.view(B * n, -1), t.proj)
 
 
 @dataclasses.dataclass
@@ -55,6 +125,7 @@ class Models:
     absolute position (mod P).  last0, len0: [B] int32 start state (last
     committed token, committed length).  u_accept [R, B, gamma] and
     u_sample [R, B, gamma+1]: float32 uniforms of each round.  T: temperature.
+    attention: None, or the target's attention layer.
     """
     draft_table: object
     target_table: object
@@ -64,6 +135,7 @@ class Models:
     u_accept: object
     u_sample: object
     T: float
+    attention: TargetAttention | None = None
 
     @property
     def B(self) -> int:
@@ -110,6 +182,7 @@ class _Buffers:
         self.p = [rows(), rows()]
         self.q = [rows(), rows()]
         self.out = [alloc_outputs(B, g, dev) for _ in range(rounds)]
+        self.attention = None if m.attention is None else _Attention(m.attention, m, rounds)
         if ssd:
             self.ws_p = new_workspace(spec_predict_workspace_bytes(B, g, V, dt), dev)
             self.pred = [alloc_predict_outputs(B, g, dev) for _ in range(rounds)]
@@ -137,6 +210,8 @@ def run_sd(m: Models, rounds: int, t_draft_ns: int, t_target_ns: int):
             spec_synthetic_busy(t_draft_ns, stream=st, device=dev)
             spec_synth_rows(m.draft_table, bf.last[r], bf.x[r], out=p, stream=st)
             spec_synth_rows(m.target_table, bf.last[r], bf.x[r], out=q, stream=st)
+            if bf.attention:
+                bf.attention.add_to(q, bf.last[r], bf.length[r], bf.x[r], st)
             spec_synthetic_busy(t_target_ns, stream=st, device=dev)
             out = spec_verify(p, q, bf.x[r], m.u_accept[r], m.u_sample[r], m.T,
                               in_len=bf.length[r], out=bf.out[r], workspace=bf.ws, stream=st)
@@ -166,6 +241,8 @@ def run_ssd(m: Models, rounds: int, t_draft_ns: int, t_target_ns: int, fanout: f
         with torch.cuda.stream(st_t):
             st_t.wait_event(bf.ready[r])
             spec_synth_rows(m.target_table, last, x, out=q, stream=st_t)
+            if bf.attention:
+                bf.attention.add_to(q, last, length, x, st_t)
             spec_synthetic_busy(t_target_ns, stream=st_t, device=dev)
             out, pred = spec_verify_predict(p, q, x, m.u_accept[r], m.u_sample[r], m.T,
                                             in_len=length, out=bf.out[r], pred=bf.pred[r],
