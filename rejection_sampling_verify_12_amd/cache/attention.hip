@@ -51,7 +51,7 @@ struct AttentionArgs {
   void* out;
   float* lse;
   struct Join* joins;   // [grid]
-  float* parts;         // [2 * grid]: a part's numbers [rows][D], references [rows], sums [rows]
+  float* parts;         // [2 * grid]: a part's numbers [rows][D], references [rows], sums to divide by [rows], sums for lse [rows]
 };
 
 // An item that several runs hold, written by the second of them (parts = 0 by
@@ -65,7 +65,7 @@ constexpr int kTerms = DT == kBF16 ? 1 : 3;   // bfloat16 parts that a query or 
 
 // Waves per SIMD the registers of a variant leave room for.
 constexpr int waves_for(int D, int dt, int rt) {
-  const int regs = rt * (D / 4 + 16) + D / 2 + 36;
+  const int regs = rt * (D / 4 + 16) + D / 2 + 42;
   return regs <= 128 ? 4 : regs <= 168 ? 3 : 2;
 }
 // Row tiles of a group, at most.
@@ -230,7 +230,12 @@ constexpr float kNone = -FLT_MAX;
 template <int D, int DT, int RT>
 struct State {   // one wave's running result; a lane holds query (lane & 15) of each tile
   f32x4 o[RT][D / 16];
-  float m[RT], l[RT];   // reference (base 2; kNone before the first key), and the sum over the lane's own keys
+  float m[RT];   // reference (base 2; kNone before the first key)
+  float l[RT];   // sum of the weights over the lane's own keys; bf16: only if lse is wanted
+  // bf16: sum of the rounded weights over all keys, by a product with ones.
+  // Dividing by it rather than by l cancels the part of the roundings that
+  // the weights have in common (all of it where one weight carries the row).
+  f32x4 r[DT == kBF16 ? RT : 1];
 };
 
 // Whether a group's queries are kept in shared memory (else in registers).
@@ -319,7 +324,7 @@ __device__ __forceinline__ uint32_t seen_keys(const AttentionArgs& a, const Item
 // Weights of a block and the running maximum and sum.  `masked`: some row does not see some key.
 template <int D, int DT, int RT>
 __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& it, int b, int p, int lane, bool masked,
-                                            uint32_t nan_keys, float c2, const Rows<D, DT, RT>& rows, f32x4 (&s)[RT][2],
+                                            uint32_t nan_keys, float c2, bool lse, const Rows<D, DT, RT>& rows, f32x4 (&s)[RT][2],
                                             State<D, DT, RT>& st, bf16x8 (&w)[RT][kTerms<DT>]) {
   const int g = lane >> 4;
 #pragma unroll
@@ -349,13 +354,14 @@ __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& 
       top = swap_combine<32>(swap_combine<16>(top, maxf), maxf) * c2;
       const float m = fmaxf(st.m[rt], top), alpha = exp2_fast(st.m[rt] - m);
       st.l[rt] *= alpha;
+      if constexpr (DT == kBF16) st.r[rt] *= alpha;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) st.o[rt][d] *= alpha;
       st.m[rt] = m;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = exp2_fast(fmaf(x[e], c2, -st.m[rt]));
-    st.l[rt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    if (DT == kF32 || lse) st.l[rt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     split8<kTerms<DT>>(x, w[rt]);
   }
 }
@@ -365,6 +371,11 @@ __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& 
 template <int D, int DT, int RT>
 __device__ __forceinline__ void gather_block(const Half<D>& x, const bf16x8 (&w)[RT][kTerms<DT>], State<D, DT, RT>& st) {
   constexpr int T = kTerms<DT>;
+  if constexpr (DT == kBF16) {
+    const bf16x8 ones = as_bf16x8(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) st.r[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, w[rt][0], st.r[rt], 0, 0, 0);
+  }
   float sc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sc[e] = scale_of(__builtin_amdgcn_ubfe(x.sc[e >> 2], 8 * (e & 3), 8));
@@ -454,10 +465,10 @@ __device__ __forceinline__ V pin(V x) {
 template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kernel(AttentionArgs) {
   const AttentionArgs& a = kernel_arg0<AttentionArgs>();
-  constexpr int R = 16 * RT, S = D / 16, kPart = R * (D + 2), T = kTerms<DT>;
+  constexpr int R = 16 * RT, S = D / 16, kPart = R * (D + 3), T = kTerms<DT>;
   constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = kQueriesShared<DT, RT> ? R * D * 2 * T : 0;
   __shared__ __align__(16) char space[kSums > kQ ? kSums : kQ];   // the queries, then the waves' results
-  __shared__ float tops[kWaves][R], totals[kWaves][R];
+  __shared__ float tops[kWaves][R], totals[kWaves][R], exacts[kWaves][R];   // references, sums to divide by, sums for lse
   __shared__ Span spans[kSpans];
   float (&sums)[kWaves][16][D + 4] = *reinterpret_cast<float (*)[kWaves][16][D + 4]>(space);
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -554,6 +565,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     const uint8_t* head = pin(a.c.data + (int64_t)h * record);
     const int64_t page_bytes = (int64_t)heads * record;
     const float c2 = pin(a.c2);
+    const bool lse = a.lse != nullptr;
     const int p1 = min(it.hi, it.lo + kUnitKeys * k1);
     int p = it.lo + kUnitKeys * k0 + kBlock * wave;
     // Blocks from whole0 to whole1 are seen by every row as a whole.
@@ -604,6 +616,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       }
       st.m[rt] = kNone;
       st.l[rt] = 0.0f;
+      if constexpr (DT == kBF16) st.r[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int d = 0; d < S; ++d) st.o[rt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -643,7 +656,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
             if ((x >> (8 * (e & 3)) & 255) > 252) x = (x & ~(255u << (8 * (e & 3)))) | 127u << (8 * (e & 3));
           }
         }
-        weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, c2, rows, s, st, w);
+        weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, c2, lse, rows, s, st, w);
         __builtin_amdgcn_sched_barrier(0);
         gather_block<D, DT, RT>(v0, w, st);
         __builtin_amdgcn_sched_barrier(0);
@@ -661,7 +674,8 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       st.l[rt] = swap_combine<32>(swap_combine<16>(st.l[rt], add2), add2);
       if (g == 0) {
         tops[wave][rt * 16 + i] = st.m[rt];
-        totals[wave][rt * 16 + i] = st.l[rt];
+        totals[wave][rt * 16 + i] = DT == kBF16 ? st.r[rt][0] : st.l[rt];
+        exacts[wave][rt * 16 + i] = st.l[rt];
       }
     }
     __syncthreads();
@@ -683,11 +697,15 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       __syncthreads();
       const int row16 = tid >> 4, share = tid & 15, r = rt * 16 + row16;
       if (r < used) {
-        float m = tops[0][r], l = 0.0f, v[S];
+        float m = tops[0][r], l = 0.0f, exact = 0.0f, v[S];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][r]);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) l += totals[w][r] * exp2_fast(tops[w][r] - m);
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = exp2_fast(tops[w][r] - m);
+          l += totals[w][r] * f;
+          exact += exacts[w][r] * f;
+        }
 #pragma unroll
         for (int d = 0; d < S; ++d)
           v[d] = (sums[0][row16][share * S + d] + sums[1][row16][share * S + d]) + (sums[2][row16][share * S + d] + sums[3][row16][share * S + d]);
@@ -697,13 +715,14 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
 #pragma unroll
           for (int d = 0; d < S; ++d) v[d] *= inv;
           store_numbers<D, DT, S>(a.out, at * D + share * S, v);
-          if (a.lse && share == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          if (a.lse && share == 0) a.lse[at] = exact == 0.0f ? -INFINITY : (m + log2f(exact)) * 0.6931471805599453f;
         } else {
 #pragma unroll
           for (int d = 0; d < S; d += 4) *reinterpret_cast<f32x4*>(part + r * D + share * S + d) = f32x4{v[d], v[d + 1], v[d + 2], v[d + 3]};
           if (share == 0) {
             part[R * D + r] = m;
             part[R * D + R + r] = l;
+            part[R * D + 2 * R + r] = exact;
           }
         }
       }
@@ -722,22 +741,23 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
 template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
   const AttentionArgs& a = kernel_arg0<AttentionArgs>();
-  constexpr int R = 16 * RT, kPart = R * (D + 2), kLanes = D / 4, kSplit = 64 / kLanes, kAhead = 8;
+  constexpr int R = 16 * RT, kPart = R * (D + 3), kLanes = D / 4, kSplit = 64 / kLanes, kAhead = 8;
   const Join j = a.joins[blockIdx.x];
   const int lane = threadIdx.x & 63, r = blockIdx.y * kWaves + uni((int)(threadIdx.x >> 6));
   if (r >= (j.parts > 0 ? j.used : 0)) return;
   const int first = (int)blockIdx.x - 1, mine = lane / kLanes, d = lane % kLanes * 4;
   const auto part_at = [&](int x) { return a.parts + (int64_t)(2 * (first + x) + (x == 0 ? j.side : 0)) * kPart; };
-  float m = kNone, l = 0.0f;
+  float m = kNone, l = 0.0f, exact = 0.0f;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int x = mine; x < j.parts; x += kSplit * kAhead) {
-    float pm[kAhead], pl[kAhead];
+    float pm[kAhead], pl[kAhead], pe[kAhead];
     f32x4 pv[kAhead];
 #pragma unroll
     for (int y = 0; y < kAhead; ++y) {
       const float* p = part_at(min(x + y * kSplit, j.parts - 1));
       pm[y] = p[R * D + r];
       pl[y] = p[R * D + R + r];
+      pe[y] = p[R * D + 2 * R + r];
       pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + d);
     }
     float top = m;
@@ -746,12 +766,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
     const float f0 = exp2_fast(m - top);
     m = top;
     l *= f0;
+    exact *= f0;
     v *= f0;
 #pragma unroll
     for (int y = 0; y < kAhead; ++y) {
       if (x + y * kSplit < j.parts) {
         const float f = exp2_fast(pm[y] - top);
         l += pl[y] * f;
+        exact += pe[y] * f;
         v += pv[y] * f;
       }
     }
@@ -762,6 +784,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
     const float top = swap_combine<decltype(swap)::value>(m, max2), f = exp2_fast(m - top);
     m = top;
     l = swap_combine<decltype(swap)::value>(l * f, add2);
+    exact = swap_combine<decltype(swap)::value>(exact * f, add2);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = swap_combine<decltype(swap)::value>(v[e] * f, add2);
   };
@@ -773,7 +796,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
   store_numbers<D, DT, 4>(a.out, at * D + d, o);
-  if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  if (a.lse && d == 0) a.lse[at] = exact == 0.0f ? -INFINITY : (m + log2f(exact)) * 0.6931471805599453f;
 }
 
 int check_attention(int B, int n, int heads_q, int heads, int dim) {
@@ -802,7 +825,7 @@ extern "C" size_t spec_cache_attention_workspace_bytes(int B, int n, int heads_q
   for (int dt : {(int)kF32, (int)kBF16}) {
     const int64_t tiles = ((int64_t)n * (heads_q / heads) + 15) / 16;
     for (int rt = 1; rt <= max_tiles(dim, dt) && rt <= tiles; ++rt) {
-      const size_t need = (size_t)2 * grid_for(dim, dt, rt) * 16 * rt * (dim + 2) * sizeof(float);
+      const size_t need = (size_t)2 * grid_for(dim, dt, rt) * 16 * rt * (dim + 3) * sizeof(float);
       parts = need > parts ? need : parts;
     }
   }

@@ -16,8 +16,9 @@ float32).  With A = sum w |v| / sum w and S1 = the largest scale * sum |q k|:
   and so the quotient by 4 delta A;
 * T weights are summed for the numerator and for the denominator, and partial
   sums rescaled and joined: 2 (T + 40) u A;
-* bfloat16: the weights are rounded before the product, h A; the output is
-  rounded, h |out|.  float32: queries and weights are each cut into three
+* bfloat16: both sums take the rounded weights w (1 + d), |d| <= h, which
+  moves the quotient by sum w d (v - out) / sum w (1 + d), at most
+  h (A + |out|) up to h squared; the output is rounded, h |out|.  float32: queries and weights are each cut into three
   bfloat16 parts, which leaves at most 2^-24 of them: u S1 in the score, u A.
 * lse: delta + (T + 40) u + 2 u |lse|.
 """
@@ -296,7 +297,7 @@ def check_attention(pool, q, got, first, counts, scale, window=0, mask=None, row
             continue
         T = len(K)
         delta = (dim + 8) * U * S1 + 4 * U * r + 8 * U + (0 if bf else U * S1)
-        tol = (4 * delta + 2 * (T + 40) * U + (h if bf else U)) * A + h * np.abs(o) + 1e-37
+        tol = (4 * delta + 2 * (T + 40) * U + (h if bf else U)) * A + (2 * h if bf else h) * np.abs(o) + 1e-37
         err = np.abs(out[b, i, c] - o)
         assert (err <= tol).all(), f"{where}: off by {np.max(err / tol):.3g} bounds"
         worst = max(worst, float(np.max(err / tol)))
