@@ -464,11 +464,13 @@ int spec_lds_atomic_probe(int pattern, int iters, uint64_t* sink, void* stream);
  * are neither read nor written.
  *
  * Errors.  B < 0, n < 1, heads < 1, pages < 0, table_len < 0, a page or dim
- * that is not listed, table_len * page > 2^30, B * n > 2^24, sizes whose work
- * items do not fit 31 bits (B * n * heads_q * dim > 2^34; B * heads * row groups of 16 > 2^24), a
- * negative stride, lag outside {0, 1}, a NULL required pointer, `data` or an output off its
- * 16-byte boundary: SPEC_EINVAL; an unknown dtype: SPEC_EDTYPE.  B == 0 is a
- * no-op.  Found on the device, and confined to the sequence: a
+ * that is not listed, table_len * page > 2^30, B * n > 2^24, B * n * heads *
+ * dim > 2^34 (heads_q for the attention), a negative stride, lag outside
+ * {0, 1}, a NULL required pointer, `data` or an output off its 16-byte
+ * boundary: SPEC_EINVAL; an unknown dtype: SPEC_EDTYPE.  B == 0 is a no-op.
+ * The attention's work items must fit 31 bits too: B * heads * ceil(n * group
+ * / 16) <= 2^24, n * group^2 < 2^32 and B * heads * ceil(n * group / 16) *
+ * (table_len * page / 128 + 8) < 2^31, group = heads_q / heads.  Found on the device, and confined to the sequence: a
  * first position below 0, a count outside [0, n], or tokens past
  * table_len * page positions (a range error), and a page outside [0, pages).
  *
@@ -495,7 +497,7 @@ int spec_lds_atomic_probe(int pattern, int iters, uint64_t* sink, void* stream);
  *   a whole, as are all n rows after a range error; what a row does not see
  *   never reaches it.
  *   q: [B][n][heads_q][dim] of dtype, tokens q_stride elements apart;
- *   heads_q: a multiple of heads; scale finite;
+ *   heads_q: a multiple of heads; scale finite, below 2^127;
  *   out: [B][n][heads_q][dim] of dtype, contiguous; lse: [B][n][heads_q] float
  *   (nullable).  Outputs must not overlap inputs.
  *   Scores, the softmax's maximum and sum and the output are held in 32 bits;

@@ -17,6 +17,20 @@
 // a query after the first product needs exactly those 8 keys in the second, so
 // the weights never move between lanes.  Column = query in both products, so
 // the softmax's maximum, sum and rescaling are one register per lane.
+//
+// What bounds it.  Few rows (plain decoding): reading the cache.  64
+// sequences of 2000 to 33000 positions, 8 heads of 128, 8 query rows each:
+// 777 MB in 130 us, 6.0 TB/s in all and 6.9 TB/s in the loop, where a plain
+// read reaches 7.2.  Many rows (verification, prompts): the vector
+// instructions and the latency between dependent ones.  A block of 32 keys at
+// dim 128 takes 112 of them to turn the codes into bfloat16 (a value's codes
+// come in pairs along the vector and are needed in pairs along the keys: one
+// v_perm per pair, as each token has its own scale), and about 45 and 17 matrix
+// products of 16 cycles for each tile of 16 queries.  256 sequences of 300 to
+// 6000 positions, 36 rows per head: 568 MB in 165 us, against 79 us at the
+// read rate.  Measured and left: key codes straight into the scaled 4-bit
+// by 8-bit matrix product (the queries as two 8-bit parts) saves 34
+// instructions a block, but its sums keep only about 17 bits below the largest term.
 #include "format.h"
 
 #include <float.h>
@@ -33,7 +47,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 32;               // keys per wave and step
 constexpr int kUnitKeys = kWaves * kBlock;   // keys per work-group and step
-constexpr int kItemUnits = 6;
+constexpr int kItemUnits = 6;            // measured 3, 4, 6: 181, 174, 167 us for 256 sequences of 300 to 6000 positions
 constexpr int kCUs = 256;                // MI355X
 constexpr int kSpans = 512;              // sequences whose positions a work-group keeps in shared memory
 
@@ -63,12 +77,17 @@ struct Join {
 template <int DT>
 constexpr int kTerms = DT == kBF16 ? 1 : 3;   // bfloat16 parts that a query or a weight is cut into
 
-// Waves per SIMD the registers of a variant leave room for.
+// Waves per SIMD the registers of a variant leave room for (a fit to what the
+// compiler needs).  Holding every variant to two or more pays although the
+// largest two keep some of what surrounds the loop in scratch memory: prompt pieces of 2048
+// tokens 95 us against 126 with one wave.
 constexpr int waves_for(int D, int dt, int rt) {
   const int regs = rt * (D / 4 + 16) + D / 2 + 42;
   return regs <= 128 ? 4 : regs <= 168 ? 3 : 2;
 }
-// Row tiles of a group, at most.
+// Row tiles of a group, at most: the codes are turned into numbers once for
+// all of them.  (Three at dim 128 instead of four: 95 against 92 us for prompt
+// pieces; one at dim 256 instead of two: 62 against 53 us for trees of 24 tokens.)
 constexpr int max_tiles(int D, int dt) { return dt == kBF16 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2); }
 // Row tiles per group for rows of one sequence and head: as many groups as the
 // largest tile count needs, the tiles spread evenly over them.
@@ -523,7 +542,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   int entry = __builtin_amdgcn_readlane(found, at), entry_start = __builtin_amdgcn_readlane(start, at);
   const Places<D> places(1 << a.c.page_log2, lane);
 
-  while (u < u1) {
+  while (u < u1 && entry < entries) {
     const int b = entry / a.groups, rg = entry - b * a.groups;
     const Span span = span_at(b);
     const Item it = item_of(a, {uni(span.pos), uni(span.count)}, rg, R);
@@ -737,7 +756,10 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
 }
 
 // Joins the parts of the items that several runs hold, in order: a wave per
-// row, a lane 4 numbers of every (256 / D)-th part.
+// row, a lane 4 numbers of every (256 / D)-th part.  A kernel of its own
+// spreads the rows over the chip: with the last work-group to arrive joining its
+// item alone, 5 tokens over 200000 positions took 72 us and now take 55, one
+// token over 2000 positions 12.5 and now 12.
 template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
   const AttentionArgs& a = kernel_arg0<AttentionArgs>();
@@ -854,10 +876,11 @@ extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int 
   a.heads_q = heads_q;
   a.group = heads_q / cache->heads;
   const float c2 = fabsf(scale) * 1.4426950408889634f;
+  if (!isfinite(c2)) return SPEC_EINVAL;
   a.zero = c2 < FLT_MIN;
   a.c2 = a.zero ? 1.0f : c2;
   a.flip = scale < 0.0f;
-  a.window = window;
+  a.window = window < 1 << 30 ? window : 0;   // positions are below 2^30
   a.mask = mask;
   a.out = out;
   a.lse = lse;
@@ -873,12 +896,11 @@ extern "C" int spec_cache_attention(const spec_cache* cache, const void* q, int 
   const int64_t most = (int64_t)B * a.groups * cache->heads * (((int64_t)cache->table_len * cache->page + kUnitKeys - 1) / kUnitKeys + 1 + kItemUnits);
   if (most > INT_MAX) return SPEC_EINVAL;
   const unsigned row_chunks = (unsigned)((rows < 16 * rt ? rows : 16 * rt) + kWaves - 1) / kWaves;
-  const bool split = true;
 #define SV_LAUNCH(D, DT, RT)                                                                                       \
   if (cache->dim == D && dt == (int)DT && rt == RT) {                                                              \
     const int grid = (int)(most < grid_for(D, DT, RT) ? most : grid_for(D, DT, RT));                               \
     hipLaunchKernelGGL((attention_kernel<D, DT, RT>), dim3(grid), dim3(kThreads), 0, st, a);                       \
-    if (split) hipLaunchKernelGGL((join_kernel<D, DT, RT>), dim3(grid, row_chunks), dim3(kThreads), 0, st, a);     \
+    hipLaunchKernelGGL((join_kernel<D, DT, RT>), dim3(grid, row_chunks), dim3(kThreads), 0, st, a);     \
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ELAUNCH;                                               \
   }
   SV_LAUNCH(64, kBF16, 1) SV_LAUNCH(64, kBF16, 2) SV_LAUNCH(64, kBF16, 3) SV_LAUNCH(64, kBF16, 4)

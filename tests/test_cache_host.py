@@ -66,7 +66,7 @@ def test_read_refuses():
 
 def test_attention_refuses():
     for kw in (dict(q=None), dict(out=None), dict(qs=-1), dict(q=FAKE + 1), dict(out=FAKE + 8), dict(heads_q=0),
-               dict(heads_q=3), dict(heads_q=1), dict(heads_q=-2), dict(scale=math.nan), dict(scale=math.inf),
+               dict(heads_q=3), dict(heads_q=1), dict(heads_q=-2), dict(scale=math.nan), dict(scale=math.inf), dict(scale=3.2e38),
                dict(window=-1), dict(n=65, mask=FAKE), dict(heads_q=1 << 30)):
         assert attention(**kw) == R.SPEC_EINVAL, kw
     assert attention(ws=None) == R.SPEC_EWORKSPACE

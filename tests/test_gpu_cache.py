@@ -354,7 +354,30 @@ def test_attention(case, lag):
     run_case(np.random.default_rng(sum(case[:6])), *case, lag=lag)
 
 
-@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 5000])
+def test_more_sequences_than_shared_memory_holds():
+    """Positions of 700 sequences, some without tokens; and 99 row groups of three prompts."""
+    H.say("[cache] 700 sequences")
+    rng = np.random.default_rng(21)
+    rows = [(b, 0, c) for b in list(range(0, 700, 23)) + [510, 511, 512, 513, 699] for c in (0, 1)]
+    run_case(rng, 700, 1, 1, 2, 64, 32, "bf16", [(37 * b) % 90 for b in range(700)], counts=[int(b % 5 != 2) for b in range(700)], rows=rows)
+    rows = [(b, i, c) for b in range(3) for i in (0, 1, 21, 22, 340, 698, 699) for c in (0, 5)]
+    run_case(rng, 3, 700, 2, 3, 128, 64, "bf16", [0, 33, 400], counts=[700, 23, 699], rows=rows)
+
+
+def test_calls_without_tokens_write_nothing():
+    H.say("[cache] no tokens")
+    run_case(np.random.default_rng(22), 3, 2, 1, 2, 64, 32, "f32", [5, 0, 40], counts=[0, 0, 0])
+
+
+def test_the_workspace_may_hold_anything():
+    H.say("[cache] workspace of NaN bytes")
+    n = R.spec_cache_attention_workspace_bytes(2, 9, 8, 2, 128)
+    for byte in (0xFF, 0x7F):
+        ws = torch.full((n,), byte, dtype=torch.uint8, device="cuda")
+        run_case(np.random.default_rng(23), 2, 9, 2, 4, 128, 64, "bf16", [0, 1500], workspace=ws)
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 5000, 2 ** 31 - 1])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_window(window, dt):
     H.say(f"[cache] window {window} {dt}")
