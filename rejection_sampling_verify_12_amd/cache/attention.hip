@@ -755,70 +755,112 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   }
 }
 
-// Joins the parts of the items that several runs hold, in order: a wave per
-// row, a lane 4 numbers of every (256 / D)-th part.  A kernel of its own
-// spreads the rows over the chip: with the last work-group to arrive joining its
-// item alone, 5 tokens over 200000 positions took 72 us and now take 55, one
-// token over 2000 positions 12.5 and now 12.
+// Joins the parts of the items that several runs hold, in order.  A wave takes
+// kRows rows, a lane 4 numbers of every (256 / D)-th part; where an item has
+// many parts the waves of a work-group share them, and the work-group takes
+// kRows rows.  A kernel of its own spreads the rows over the chip: with the
+// last work-group to arrive joining its item alone, 5 tokens over 200000
+// positions took 72 us and now take 51.
 template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs) {
   const AttentionArgs& a = kernel_arg0<AttentionArgs>();
-  constexpr int R = 16 * RT, kPart = R * (D + 3), kLanes = D / 4, kSplit = 64 / kLanes, kAhead = 8;
-  const Join j = a.joins[blockIdx.x];
-  const int lane = threadIdx.x & 63, r = blockIdx.y * kWaves + uni((int)(threadIdx.x >> 6));
-  if (r >= (j.parts > 0 ? j.used : 0)) return;
-  const int first = (int)blockIdx.x - 1, mine = lane / kLanes, d = lane % kLanes * 4;
-  const auto part_at = [&](int x) { return a.parts + (int64_t)(2 * (first + x) + (x == 0 ? j.side : 0)) * kPart; };
-  float m = kNone, l = 0.0f, exact = 0.0f;
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int x = mine; x < j.parts; x += kSplit * kAhead) {
-    float pm[kAhead], pl[kAhead], pe[kAhead];
-    f32x4 pv[kAhead];
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      const float* p = part_at(min(x + y * kSplit, j.parts - 1));
-      pm[y] = p[R * D + r];
-      pl[y] = p[R * D + R + r];
-      pe[y] = p[R * D + 2 * R + r];
-      pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + d);
+  constexpr int R = 16 * RT, kPart = R * (D + 3), kLanes = D / 4, kSplit = 64 / kLanes, kAhead = 4, kRows = 4;
+  static_assert(kRows == kWaves, "a wave joins one row of a shared item");
+  __shared__ f32x4 numbers[kWaves][kRows][kLanes];
+  __shared__ float sums[kWaves][kRows][3];
+  const int* at = reinterpret_cast<const int*>(a.joins + blockIdx.x);
+  const Join j = {scalar_at(at, 0), scalar_at(at, 1), scalar_at(at, 2), scalar_at(at, 3), scalar_at(at, 4), scalar_at(at, 5)};
+  const bool shared = j.parts > 4 * kSplit;
+  const int lane = threadIdx.x & 63, wave = uni((int)(threadIdx.x >> 6)), rows = shared ? kRows : kRows * kWaves;
+  if (j.parts == 0 || (int)blockIdx.y * rows >= j.used) return;   // the whole work-group
+  const int r0 = (int)blockIdx.y * rows + (shared ? 0 : wave * kRows), first = (int)blockIdx.x - 1;
+  const int mine = lane / kLanes + (shared ? wave * kSplit : 0), step = shared ? kWaves * kSplit : kSplit, d = lane % kLanes * 4;
+  struct Sum {
+    float m, l, exact;
+    f32x4 v;
+    __device__ __forceinline__ void add(float pm, float pl, float pe, f32x4 pv) {
+      const float top = fmaxf(m, pm), f0 = exp2_fast(m - top), f1 = exp2_fast(pm - top);
+      m = top;
+      l = l * f0 + pl * f1;
+      exact = exact * f0 + pe * f1;
+      v = v * f0 + pv * f1;
     }
-    float top = m;
+  };
+  Sum sum[kRows];
 #pragma unroll
-    for (int y = 0; y < kAhead; ++y) top = fmaxf(top, pm[y]);
-    const float f0 = exp2_fast(m - top);
-    m = top;
-    l *= f0;
-    exact *= f0;
-    v *= f0;
+  for (int n = 0; n < kRows; ++n) sum[n] = {kNone, 0.0f, 0.0f, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+  for (int x = mine; x < j.parts; x += step * kAhead) {
+    float pm[kAhead][kRows], pl[kAhead][kRows], pe[kAhead][kRows];
+    f32x4 pv[kAhead][kRows];
 #pragma unroll
     for (int y = 0; y < kAhead; ++y) {
-      if (x + y * kSplit < j.parts) {
-        const float f = exp2_fast(pm[y] - top);
-        l += pl[y] * f;
-        exact += pe[y] * f;
-        v += pv[y] * f;
+      const int z = x + y * step;
+      const float* p = a.parts + (int64_t)(2 * (first + z) + (z == 0 ? j.side : 0)) * kPart;
+#pragma unroll
+      for (int n = 0; n < kRows; ++n) {
+        const int r = r0 + n;
+        pm[y][n] = kNone;
+        pl[y][n] = pe[y][n] = 0.0f;
+        pv[y][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (z < j.parts && r < j.used) {
+          pm[y][n] = p[R * D + r];
+          pl[y][n] = p[R * D + R + r];
+          pe[y][n] = p[R * D + 2 * R + r];
+          pv[y][n] = *reinterpret_cast<const f32x4*>(p + r * D + d);
+        }
       }
     }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+      for (int n = 0; n < kRows; ++n) sum[n].add(pm[y][n], pl[y][n], pe[y][n], pv[y][n]);
   }
-  const auto join2 = [&](auto swap) {   // with the lane that has the row's other parts
+  const auto join2 = [](Sum& s, auto swap) {   // with the lane that has the row's other parts
     const auto max2 = [](float x, float y) { return fmaxf(x, y); };
     const auto add2 = [](float x, float y) { return x + y; };
-    const float top = swap_combine<decltype(swap)::value>(m, max2), f = exp2_fast(m - top);
-    m = top;
-    l = swap_combine<decltype(swap)::value>(l * f, add2);
-    exact = swap_combine<decltype(swap)::value>(exact * f, add2);
+    constexpr int kSwap = decltype(swap)::value;
+    const float top = swap_combine<kSwap>(s.m, max2), f = exp2_fast(s.m - top);
+    s.m = top;
+    s.l = swap_combine<kSwap>(s.l * f, add2);
+    s.exact = swap_combine<kSwap>(s.exact * f, add2);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = swap_combine<decltype(swap)::value>(v[e] * f, add2);
+    for (int e = 0; e < 4; ++e) s.v[e] = swap_combine<kSwap>(s.v[e] * f, add2);
   };
-  if constexpr (kSplit == 4) join2(std::integral_constant<int, 16>{});
-  if constexpr (kSplit >= 2) join2(std::integral_constant<int, 32>{});
-  if (mine > 0) return;
-  const int row = j.row0 + r, token = token_of(a, row);
-  const int64_t at = ((int64_t)j.b * a.c.n + token) * a.heads_q + j.h * a.group + (row - token * a.group);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-  store_numbers<D, DT, 4>(a.out, at * D + d, o);
-  if (a.lse && d == 0) a.lse[at] = exact == 0.0f ? -INFINITY : (m + log2f(exact)) * 0.6931471805599453f;
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    if constexpr (kSplit == 4) join2(sum[n], std::integral_constant<int, 16>{});
+    if constexpr (kSplit >= 2) join2(sum[n], std::integral_constant<int, 32>{});
+  }
+  const auto write = [&](int r, const Sum& s) {
+    const int row = j.row0 + r, token = token_of(a, row);
+    const int64_t to = ((int64_t)j.b * a.c.n + token) * a.heads_q + j.h * a.group + (row - token * a.group);
+    const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+    const float o[4] = {s.v[0] * inv, s.v[1] * inv, s.v[2] * inv, s.v[3] * inv};
+    store_numbers<D, DT, 4>(a.out, to * D + d, o);
+    if (a.lse && d == 0) a.lse[to] = s.exact == 0.0f ? -INFINITY : (s.m + log2f(s.exact)) * 0.6931471805599453f;
+  };
+  if (!shared) {
+#pragma unroll
+    for (int n = 0; n < kRows; ++n)
+      if (lane < kLanes && r0 + n < j.used) write(r0 + n, sum[n]);
+    return;
+  }
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    if (lane < kLanes) numbers[wave][n][lane] = sum[n].v;
+    if (lane == 0) {
+      sums[wave][n][0] = sum[n].m;
+      sums[wave][n][1] = sum[n].l;
+      sums[wave][n][2] = sum[n].exact;
+    }
+  }
+  __syncthreads();
+  if (lane < kLanes && r0 + wave < j.used) {
+    Sum s = {kNone, 0.0f, 0.0f, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) s.add(sums[w][wave][0], sums[w][wave][1], sums[w][wave][2], numbers[w][wave][lane]);
+    write(r0 + wave, s);
+  }
 }
 
 int check_attention(int B, int n, int heads_q, int heads, int dim) {
