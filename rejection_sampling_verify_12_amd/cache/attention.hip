@@ -27,7 +27,7 @@
 // come in pairs along the vector and are needed in pairs along the keys: one
 // v_perm per pair, as each token has its own scale), and about 45 and 17 matrix
 // products of 16 cycles for each tile of 16 queries.  256 sequences of 300 to
-// 6000 positions, 36 rows per head: 568 MB in 165 us, against 79 us at the
+// 6000 positions, 36 rows per head: 568 MB in 159 us, against 79 us at the
 // read rate.  Measured and left: key codes straight into the scaled 4-bit
 // by 8-bit matrix product (the queries as two 8-bit parts) saves 34
 // instructions a block, but its sums keep only about 17 bits below the largest term.
@@ -658,6 +658,9 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         const bool masked = p < whole0 || p > whole1;
         score_block<D, DT, RT>(k, ks, rows, lane, s);
         __builtin_amdgcn_sched_barrier(0);
+        // A wave that feeds the matrix cores goes before one that works on its
+        // weights: 256 sequences of 300 to 6000 positions 165 -> 159 us.
+        __builtin_amdgcn_s_setprio(0);
         rec = record_rsrc(head, page_bytes, more ? next : -1, record);
         load_keys<D>(rec, pn & (P - 1), places, k);
         load_values<D>(rec, pn & (P - 1), places, v1);
@@ -677,6 +680,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         }
         weigh_block<D, DT, RT>(a, it, b, p, lane, masked, nan_keys, c2, lse, rows, s, st, w);
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
         gather_block<D, DT, RT>(v0, w, st);
         __builtin_amdgcn_sched_barrier(0);
         p = pn;
@@ -684,6 +688,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       };
       while (step(v[0], v[1]) && step(v[1], v[0])) {
       }
+      __builtin_amdgcn_s_setprio(0);
     }
 
     // Join the waves.
