@@ -47,6 +47,8 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 32;               // keys per wave and step
 constexpr int kUnitKeys = kWaves * kBlock;   // keys per work-group and step
+// What an item weighs besides its units when the work is divided: queries in,
+// waves joined and results out take about as long as these units.
 constexpr int kItemUnits = 6;            // measured 3, 4, 6: 181, 174, 167 us for 256 sequences of 300 to 6000 positions
 constexpr int kCUs = 256;                // MI355X
 constexpr int kSpans = 512;              // sequences whose positions a work-group keeps in shared memory
@@ -102,10 +104,6 @@ struct Item {
   int tok0, tok1;   // its first and last token
   int lo, hi;       // positions, lo on a block's border
   int units;        // 0: no row of the group is in use
-  // What the item weighs when the work is divided: an item costs about as
-  // much time as kItemUnits units besides its keys (queries in, waves joined,
-  // results out).
-  __device__ __forceinline__ int weight() const { return units > 0 ? units + kItemUnits : 0; }
 };
 
 __device__ __forceinline__ int token_of(const AttentionArgs& a, int row) {
@@ -512,16 +510,24 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     }
   }
   const auto span_at = [&](int b) { return b < kSpans ? spans[b] : span_of(a.c, b); };
-  const auto weight_at = [&](int entry) {
+  const auto units_at = [&](int entry) {
     const int b = entry / a.groups;
-    return item_of(a, span_at(b), entry - b * a.groups, R).weight();
+    return item_of(a, span_at(b), entry - b * a.groups, R).units;
   };
-  // Weight of one head before this lane's entries, and in all (the host keeps them within 31 bits).
+  // Units of one head before this lane's entries, and in all (the host keeps
+  // them within 31 bits).  Where there is a work-group for every unit, items
+  // weigh their units alone.
   const int per = (entries + 63) / 64;
   const int e0 = min(lane * per, entries), e1 = min(e0 + per, entries);
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += weight_at(e);
-  const int through = inclusive_scan(mine), before = through - mine;
+  int units = 0, items = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int x = units_at(e);
+    units += x;
+    items += x > 0;
+  }
+  const int units_through = inclusive_scan(units), items_through = inclusive_scan(items);
+  const int extra = __builtin_amdgcn_readlane(units_through, 63) * heads <= (int)gridDim.x ? 0 : kItemUnits;
+  const int mine = units + extra * items, through = units_through + extra * items_through, before = through - mine;
   const int U = __builtin_amdgcn_readlane(through, 63) * heads, W = min(U, (int)gridDim.x), run = blockIdx.x;
   if (tid == 0) a.joins[run].parts = 0;
   if (run >= W) return;   // the whole work-group
@@ -532,7 +538,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
   const bool here = start <= u && u < through * heads;
   if (here) {
     for (int e = e0; e < e1; ++e) {
-      const int weight = weight_at(e) * heads;
+      const int x = units_at(e), weight = (x + (x > 0 ? extra : 0)) * heads;
       found = e;
       if (u < start + weight) break;
       start += weight;
@@ -546,14 +552,14 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
     const int b = entry / a.groups, rg = entry - b * a.groups;
     const Span span = span_at(b);
     const Item it = item_of(a, {uni(span.pos), uni(span.count)}, rg, R);
-    const int weight = it.weight();
+    const int weight = it.units > 0 ? it.units + extra : 0;
     if (u >= entry_start + weight * heads) {
       entry_start += weight * heads;
       ++entry;
       continue;
     }
     const int h = (u - entry_start) / weight;
-    const int u0 = entry_start + h * weight;   // the item's first unit; its last kItemUnits have no keys
+    const int u0 = entry_start + h * weight;   // the item's first unit; its last `extra` have no keys
     const int k0 = u - u0, k1 = min(u1 - u0, weight);
     const int row0 = rg * R;
     // Rows in use; all n tokens' after a range error.
