@@ -4,7 +4,7 @@
 // The query rows of one sequence that share a key/value head (n tokens times
 // heads_q / heads) are cut into groups of RT tiles of 16.  A work-group takes
 // a group and a run of keys; each of its 4 waves takes blocks of 32 keys, 4
-// blocks (a unit of 128 keys) at a time, with no shared memory in the loop:
+// blocks (a unit of 128 keys) at a time; only the queries are in shared memory:
 //
 //   S^T = K Q^T       16x16x32 products: rows = 16 keys, columns = 16 queries.
 //   P = 2^(c S - m)   c = |scale| log2 e; a lane holds 8 keys of one query.
@@ -141,15 +141,16 @@ struct Half {   // of the keys, or of the values
   uint32_t sc[2];
 };
 
+constexpr int kNT = 2;   // cache policy: nontemporal, as most calls read a key once
 template <int D>
 __device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t rs, int voff, int soff, uint32_t (&w)[D / 32]) {
   if constexpr (D == 64) {
-    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 2);
+    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, kNT);
     w[0] = t.x; w[1] = t.y;
   } else {
 #pragma unroll
     for (int x = 0; x < D / 128; ++x) {
-      const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + 16 * x, soff, 2);
+      const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + 16 * x, soff, kNT);
       w[4 * x] = t.x; w[4 * x + 1] = t.y; w[4 * x + 2] = t.z; w[4 * x + 3] = t.w;
     }
   }
@@ -255,21 +256,16 @@ struct State {   // one wave's running result; a lane holds query (lane & 15) of
   f32x4 r[DT == kBF16 ? RT : 1];
 };
 
-// Whether a group's queries are kept in shared memory (else in registers).
-template <int DT, int RT>
-constexpr bool kQueriesShared = true;
-
-template <int D, int DT, int RT>
+template <int RT>
 struct Rows {   // the group's queries
-  bf16x8 q[kQueriesShared<DT, RT> ? 1 : D / 32];
-  const u32x4* shared;   // [D / 32][RT][terms][64 lanes]
+  const u32x4* q;   // in shared memory: [D / 32][RT][terms][64 lanes]
   int token[RT];
 };
 
 // Scores of a block: rows = keys, columns = queries.  rt's tile t holds keys
 // 16 t + 4 (lane / 16) + 0 .. 3 of query lane % 16.
 template <int D, int DT, int RT>
-__device__ __forceinline__ void score_block(const Half<D>& x, const uint32_t (&ks)[2], const Rows<D, DT, RT>& rows, int lane, f32x4 (&s)[RT][2]) {
+__device__ __forceinline__ void score_block(const Half<D>& x, const uint32_t (&ks)[2], const Rows<RT>& rows, int lane, f32x4 (&s)[RT][2]) {
   constexpr int T = kTerms<DT>;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -286,12 +282,7 @@ __device__ __forceinline__ void score_block(const Half<D>& x, const uint32_t (&k
     for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
       for (int e = T - 1; e >= 0; --e) {
-        bf16x8 q;
-        if constexpr (kQueriesShared<DT, RT>) {
-          q = __builtin_bit_cast(bf16x8, rows.shared[((c * RT + rt) * T + e) * 64 + lane]);
-        } else {
-          q = rows.q[c];
-        }
+        const bf16x8 q = __builtin_bit_cast(bf16x8, rows.q[((c * RT + rt) * T + e) * 64 + lane]);
 #pragma unroll
         for (int t = 0; t < 2; ++t) s[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[t], q, s[rt][t], 0, 0, 0);
       }
@@ -341,7 +332,7 @@ __device__ __forceinline__ uint32_t seen_keys(const AttentionArgs& a, const Item
 // Weights of a block and the running maximum and sum.  `masked`: some row does not see some key.
 template <int D, int DT, int RT>
 __device__ __forceinline__ void weigh_block(const AttentionArgs& a, const Item& it, int b, int p, int lane, bool masked,
-                                            uint32_t nan_keys, float c2, bool lse, const Rows<D, DT, RT>& rows, f32x4 (&s)[RT][2],
+                                            uint32_t nan_keys, float c2, bool lse, const Rows<RT>& rows, f32x4 (&s)[RT][2],
                                             State<D, DT, RT>& st, bf16x8 (&w)[RT][kTerms<DT>]) {
   const int g = lane >> 4;
 #pragma unroll
@@ -483,7 +474,7 @@ template <int D, int DT, int RT>
 __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kernel(AttentionArgs) {
   const AttentionArgs& a = kernel_arg0<AttentionArgs>();
   constexpr int R = 16 * RT, S = D / 16, kPart = R * (D + 3), T = kTerms<DT>;
-  constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = kQueriesShared<DT, RT> ? R * D * 2 * T : 0;
+  constexpr int kSums = kWaves * 16 * (D + 4) * 4, kQ = R * D * 2 * T;
   __shared__ __align__(16) char space[kSums > kQ ? kSums : kQ];   // the queries, then the waves' results
   __shared__ float tops[kWaves][R], totals[kWaves][R], exacts[kWaves][R];   // references, sums to divide by, sums for lse
   __shared__ Span spans[kSpans];
@@ -611,9 +602,9 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       load_values<D>(rec, p & (P - 1), places, v[0]);
     }
 
-    Rows<D, DT, RT> rows;
+    Rows<RT> rows;
     State<D, DT, RT> st;
-    rows.shared = reinterpret_cast<const u32x4*>(space);
+    rows.q = reinterpret_cast<const u32x4*>(space);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int row = row0 + rt * 16 + i, token = token_of(a, row), head = h * a.group + (row - token * a.group);
@@ -622,7 +613,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
       const int64_t at = ((int64_t)b * a.c.n + token) * a.q_stride + (int64_t)head * D + g * (D / 4);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        if (kQueriesShared<DT, RT> && (rt * (D / 32) + c) % kWaves != wave) continue;   // the waves share the work
+        if ((rt * (D / 32) + c) % kWaves != wave) continue;   // the waves share the work
         float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (live) load_row8<DT>(a.q, at + 8 * c, x);
         if (a.flip) {
@@ -631,13 +622,9 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
         }
         bf16x8 q[T];
         split8<T>(x, q);
-        if constexpr (kQueriesShared<DT, RT>) {
 #pragma unroll
-          for (int e = 0; e < T; ++e)
-            reinterpret_cast<u32x4*>(space)[((c * RT + rt) * T + e) * 64 + lane] = __builtin_bit_cast(u32x4, q[e]);
-        } else {
-          rows.q[c] = q[0];
-        }
+        for (int e = 0; e < T; ++e)
+          reinterpret_cast<u32x4*>(space)[((c * RT + rt) * T + e) * 64 + lane] = __builtin_bit_cast(u32x4, q[e]);
       }
       st.m[rt] = kNone;
       st.l[rt] = 0.0f;
@@ -645,7 +632,7 @@ __global__ __launch_bounds__(kThreads, waves_for(D, DT, RT)) void attention_kern
 #pragma unroll
       for (int d = 0; d < S; ++d) st.o[rt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if constexpr (kQueriesShared<DT, RT>) __syncthreads();
+    __syncthreads();
 
     if (p < p1) {
       // One block, values in v0; the next one's go to v1.  False after the last.
